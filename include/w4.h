@@ -65,7 +65,9 @@ typedef enum {
   W4_ERR_CUDA = -5,        /* a CUDA runtime call failed; see w4_last_cuda_error()          */
   W4_ERR_TIMEOUT = -6,     /* a bounded device-side wait ran out (reported by w4_device_check) */
   W4_ERR_UNSUPPORTED = -7, /* valid arguments outside what this build implements           */
-  W4_ERR_LIMIT = -8        /* beyond the fixed size of w4_gemv_levels_noalloc's counter array */
+  W4_ERR_LIMIT = -8,       /* beyond the fixed size of w4_gemv_levels_noalloc's counter array */
+  W4_ERR_RANGE = -9        /* a page id or position held on the device is out of range (reported
+                              by w4_device_check; the access was skipped)                       */
 } w4_status;
 
 typedef enum { W4_FMT_NF4 = 0, W4_FMT_INT4 = 1, W4_FMT_FP4 = 2 } w4_format;
@@ -271,11 +273,123 @@ int w4_step_run_host(w4_step* step, const void* x_host, void* x_dev, int64_t x_b
 int w4_gemv_levels_noalloc(const w4_gemv_desc* descs, int count, w4_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
+ * Paged 8-bit key/value cache: what a decode step needs between the q/k/v projections and the o
+ * projection, and after the lm_head.
+ *
+ * A cache holds pages of `page_tokens` tokens.  A page has, for each of its kv_heads heads, a block
+ * of page_tokens x head_dim E4M3 codes for K and one for V, and one FP32 scale for each block: the
+ * value of a code is code * scale.  Sequence b's position p lies in page
+ * page_table[b * table_stride + p / page_tokens], row p % page_tokens.  Table entries that no token
+ * of a call lies in are not read as pages (any value).  A page belongs to one sequence while tokens
+ * are appended to it; reading may share pages.
+ *
+ * Batches are ragged and described on the device, so that a captured graph serves every step:
+ * sequence b's rows of q, k, v and out are q_start[b] ... q_start[b + 1] - 1 (n_b of them), and
+ * kv_len[b] is the number of tokens of the sequence INCLUDING those rows: row i of sequence b
+ * stands at position kv_len[b] - n_b + i.  A row whose position is negative is padding.
+ */
+typedef struct {
+  uint8_t* k;                 /* E4M3 codes [num_pages][kv_heads][page_tokens][head_dim]           */
+  uint8_t* v;                 /* the same shape                                                   */
+  float* k_scale;             /* [num_pages][kv_heads]; positive and finite where pages are read   */
+  float* v_scale;             /* the same                                                         */
+  const int32_t* page_table;  /* [batch][table_stride]                                            */
+  int64_t page_stride;        /* bytes from a page to the next in k and in v; 0: dense             */
+  int64_t scale_stride;       /* floats from a page to the next in the scales; 0: kv_heads         */
+  int num_pages, kv_heads;
+  int page_tokens;            /* 16, 32, 64 or 128                                                */
+  int head_dim;               /* 64 or 128                                                        */
+  int table_stride;           /* entries per sequence in page_table                               */
+} w4_kv_cache;
+
+#define W4_MAX_SEQS 1024      /* batch of w4_kv_append and w4_attn_kv8 */
+#define W4_MAX_GROUP 64       /* query heads per key/value head        */
+
+/* w4_kv_append -- rotates the new rows of q and k by their positions and appends k and v to the
+ * cache, in one launch.
+ *   rotation  the first rotary_dim channels of a head are pairs, (j, j + rotary_dim / 2), or
+ *             (2j, 2j + 1) with `interleaved`: (a, b) -> (a cos - b sin, b cos + a sin) in FP32 with
+ *             cos, sin = rope_cos, rope_sin[pos * rotary_dim / 2 + j], pos = positions[row], or the
+ *             row's position in its sequence where positions is NULL.  rotary_dim 0: no rotation.
+ *   q         rotated, rounded to FP16, written to q_out (q_out == q is allowed; NULL q and q_out:
+ *             none).  Padding rows of q_out are zero.
+ *   scale     of a page's block (a head's K, or its V): the smallest power of two s with
+ *             amax <= 448 s over the rows appended to the page since its row 0 was written, at
+ *             least 2^-60.  It only grows; when it does, the rows that the block already held are
+ *             rounded again to the new scale (exact for powers of two unless a code falls below
+ *             E4M3's normal range).  A scale that was not written by this call's rule (any positive
+ *             value) is kept as long as it is the larger.  Writing row 0 starts a page afresh.
+ *   code      E4M3(x / s), nearest even, from the FP32 value: keys are rounded once.  Infinities
+ *             become +-448; they and NaNs do not count into amax.  A token with a NaN among a head's
+ *             k or v gets NaN for that head's key and 0 for the NaN values: every query that sees
+ *             the token returns NaN, and none that does not see it is touched.
+ * max_q: at least the largest n_b.  Strides are elements from one row to the next; 0: dense
+ * (heads * head_dim).  rotary_dim: a multiple of 16, at most head_dim.  Pointers 16-byte aligned,
+ * strides multiples of 8 elements, page_stride a multiple of 16 bytes; int32 and scale pointers
+ * 4-byte aligned.  tokens may be 0.  A page id outside [0, num_pages), a position beyond the page
+ * table or a rotary position outside [0, max_position) skips the row and makes w4_device_check
+ * return W4_ERR_RANGE. */
+int w4_kv_append(const w4_kv_cache* cache, const uint16_t* q, const uint16_t* k, const uint16_t* v, uint16_t* q_out,
+                 const float* rope_cos, const float* rope_sin, const int32_t* positions, const int32_t* q_start,
+                 const int32_t* kv_len, int tokens, int batch, int q_heads, int max_q, int max_position,
+                 int rotary_dim, int interleaved, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                 int64_t q_out_stride, w4_stream_t stream);
+
+/* w4_attn_kv8 -- attention of the new rows over the cache (their own tokens appended before).  Query
+ * head h reads key/value head h / (q_heads / kv_heads).  A row at position p sees the keys j with
+ * 0 <= j < kv_len, j <= p if `causal`, and j > p - window if window > 0:
+ *   out = sum_j w_j v_j / sum_j w_j,  w_j = exp(softmax_scale q . k_j),  lse = ln sum_j w_j
+ * (lse may be NULL).  A row that sees no key (padding, an empty sequence) gets out = 0 and
+ * lse = -infinity.  Products are FP16 x FP16 -> FP32 (codes are exact in FP16), the softmax, its sums
+ * and the output are FP32, weights are rounded to FP16 for the product with V, out to FP16.
+ * One launch for every mix of lengths; the split over the keys is decided on the device from
+ * q_start and kv_len, and the pieces are joined in a fixed order (repeated calls give the same
+ * bits).  max_q: at least the largest n_b.  workspace: w4_attn_workspace_bytes(...) bytes of device
+ * memory, 16-byte aligned, zeroed by the caller before its first use and left ready for the next call
+ * by each call; calls that overlap on the GPU need one each.  q, out 16-byte aligned, strides
+ * multiples of 8 elements, page_stride a multiple of 16 bytes.  A page id outside [0, num_pages)
+ * gives an unspecified output and W4_ERR_RANGE from w4_device_check. */
+int64_t w4_attn_workspace_bytes(int tokens, int batch, int q_heads, int kv_heads, int head_dim);
+int w4_attn_kv8(const w4_kv_cache* cache, const uint16_t* q, uint16_t* out, float* lse, const int32_t* q_start,
+                const int32_t* kv_len, int tokens, int batch, int q_heads, int max_q, float softmax_scale, int causal,
+                int window, int64_t q_stride, int64_t out_stride, void* workspace, int64_t workspace_bytes,
+                w4_stream_t stream);
+
+/* w4_spec_verify -- verification of drafted tokens (speculative sampling) from logits and given
+ * random numbers.  Sequence b has n = drafts tokens drafted (n = n_drafts[b], clamped to
+ * [0, drafts], where n_drafts is not NULL).
+ *   target  FP16 logits [batch][drafts + 1][vocab], target_stride elements from row to row (0: vocab)
+ *   draft   the draft model's logits [batch][drafts][vocab], draft_stride; NULL: the drafts are
+ *           certain (copied from the context, or greedy)
+ *   u       [batch][drafts] uniform in [0, 1);  e  [batch][vocab] exponentially distributed, > 0
+ * With p_i = softmax(target_i / temperature) and q_i = softmax(draft_i / temperature) (1 at the
+ * drafted token where draft is NULL), drafted token x_i is accepted while u_i q_i(x_i) < p_i(x_i).
+ * At the first refused i the new token is argmax_v max(p_i - q_i, 0)(v) / e(v), a draw from the
+ * residual distribution by an exponential race (p_i / e where the residual is zero everywhere); after
+ * n accepted ones it is argmax_v p_n(v) / e(v).  temperature 0: x_i is accepted while it is the
+ * argmax of target_i, the new token is that argmax; u, e and draft are not read (may be NULL).  Ties
+ * go to the lowest token.  A drafted token outside [0, vocab) is refused.  A logit of -infinity or
+ * NaN stands for probability 0, +infinity for 65504.
+ *   tokens    [batch][drafts + 1]: the accepted ones, the new one (-1 if no token has a positive
+ *             probability), then -1;  accepted  [batch]: how many were accepted
+ *   logprob   [batch][drafts + 1] or NULL: ln p_i(token) (temperature 1 where temperature is 0), 0 after
+ *             the new token
+ * 1 <= drafts <= W4_MAX_DRAFTS, 1 <= vocab <= 2^24.  Pointers aligned to their element.  workspace as
+ * for w4_attn_kv8, w4_spec_verify_workspace_bytes(...) bytes. */
+#define W4_MAX_DRAFTS 31
+int64_t w4_spec_verify_workspace_bytes(int batch, int drafts, int vocab);
+int w4_spec_verify(const uint16_t* target, const uint16_t* draft, const int32_t* draft_tokens, const float* u,
+                   const float* e, int32_t* tokens, int32_t* accepted, float* logprob, int batch, int drafts,
+                   int vocab, float temperature, const int32_t* n_drafts, int64_t target_stride,
+                   int64_t draft_stride, void* workspace, int64_t workspace_bytes, w4_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
  * Diagnostics. */
 const char* w4_status_str(int status);
 int w4_last_cuda_error(void);          /* cudaError_t of the last W4_ERR_CUDA in this thread */
 /* Synchronises `stream`, reads and clears the device error word of the current device:
- * W4_OK, or W4_ERR_TIMEOUT if a bounded device-side wait ran out since the last check. */
+ * W4_OK, W4_ERR_TIMEOUT if a bounded device-side wait ran out since the last check, or W4_ERR_RANGE
+ * if a page id or position held on the device was out of range. */
 int w4_device_check(w4_stream_t stream);
 /* Kernel launches the library has issued in this process (for launch accounting). */
 long long w4_launch_count(void);

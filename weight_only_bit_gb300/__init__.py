@@ -9,9 +9,10 @@ from __future__ import annotations
 
 import ctypes
 
-from ._lib import (GemvDesc, GemvPlan, W4Error, lib, SYMBOLS, W4_OK, W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ALIGN,
+from ._lib import (GemvDesc, GemvPlan, KvCache, W4Error, lib, SYMBOLS, W4_OK, W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_ALIGN,
                    W4_ERR_BLOCKSIZE, W4_ERR_CUDA, W4_ERR_TIMEOUT, W4_ERR_UNSUPPORTED, W4_FMT_NF4,
-                   W4_FMT_INT4, W4_FMT_FP4, W4_MAX_BATCH, W4_MAX_K, W4_KERNEL_SMALL_BATCH, W4_KERNEL_TCGEN05)
+                   W4_FMT_INT4, W4_FMT_FP4, W4_MAX_BATCH, W4_MAX_K, W4_KERNEL_SMALL_BATCH, W4_KERNEL_TCGEN05,
+                   W4_ERR_LIMIT, W4_ERR_RANGE, W4_MAX_SEQS, W4_MAX_GROUP, W4_MAX_DRAFTS)
 
 __all__ = [
     "w4_nf4_codebook", "w4_quantize_nf4", "w4_quantize_int4", "w4_dequantize_nf4", "w4_dequantize_int4",
@@ -20,6 +21,8 @@ __all__ = [
     "w4_step_destroy", "w4_status_str", "w4_last_cuda_error", "w4_device_check", "w4_launch_count",
     "w4_inject_timeout_once", "w4_gemv_levels_noalloc", "w4_gemv_plan",
     "w4_quantize_fp4", "w4_dequantize_fp4", "w4_gemv_fp4", "w4_step_run_host",
+    "w4_kv_cache", "w4_kv_append", "w4_attn_workspace_bytes", "w4_attn_kv8", "w4_spec_verify_workspace_bytes",
+    "w4_spec_verify", "KvCache", "W4_ERR_RANGE", "W4_MAX_SEQS", "W4_MAX_GROUP", "W4_MAX_DRAFTS",
     "check", "W4Error", "GemvDesc", "GemvPlan", "W4_FMT_NF4", "W4_FMT_INT4", "W4_FMT_FP4", "W4_MAX_BATCH",
     "W4_MAX_K",
     "W4_KERNEL_SMALL_BATCH", "W4_KERNEL_TCGEN05",
@@ -169,3 +172,61 @@ def w4_gemv_levels_noalloc(descs, stream=None) -> int:
     that cannot allocate device memory; see include/w4.h for its limits and its one-time set-up."""
     arr = _descs(descs)
     return lib().w4_gemv_levels_noalloc(arr, len(descs), _stream(stream))
+
+
+# ---------------------------------------------------------------- paged 8-bit cache, attention, drafts
+
+
+def _nbytes(workspace, given):
+    if given is not None:
+        return given
+    if workspace is None:
+        return 0
+    if isinstance(workspace, int):
+        raise W4Error(W4_ERR_SHAPE, "a workspace given as an address needs workspace_bytes")
+    return workspace.numel() * workspace.element_size()
+
+
+def w4_kv_cache(k, v, k_scale, v_scale, page_table, *, num_pages, kv_heads, page_tokens, head_dim, table_stride,
+                page_stride=0, scale_stride=0):
+    """The cache descriptor that w4_kv_append and w4_attn_kv8 take (w4_kv_cache of include/w4.h); it
+    keeps the tensors it was made of."""
+    c = KvCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), page_stride, scale_stride, num_pages,
+                kv_heads, page_tokens, head_dim, table_stride)
+    c.tensors = (k, v, k_scale, v_scale, page_table)
+    return c
+
+
+def w4_kv_append(cache, q, k, v, q_out, rope_cos, rope_sin, q_start, kv_len, tokens, batch, q_heads, max_q,
+                 max_position, rotary_dim, interleaved=0, positions=None, q_stride=0, k_stride=0, v_stride=0,
+                 q_out_stride=0, stream=None):
+    """Rotates q and k, appends k and v to the cache; strides are elements from row to row (0: dense)."""
+    return lib().w4_kv_append(cache, _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(rope_cos), _ptr(rope_sin),
+                              _ptr(positions), _ptr(q_start), _ptr(kv_len), tokens, batch, q_heads, max_q, max_position,
+                              rotary_dim, int(interleaved), q_stride, k_stride, v_stride, q_out_stride, _stream(stream))
+
+
+def w4_attn_workspace_bytes(tokens: int, batch: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return lib().w4_attn_workspace_bytes(tokens, batch, q_heads, kv_heads, head_dim)
+
+
+def w4_attn_kv8(cache, q, out, lse, q_start, kv_len, tokens, batch, q_heads, max_q, softmax_scale, workspace, causal=1,
+                window=0, q_stride=0, out_stride=0, workspace_bytes=None, stream=None):
+    """Attention of the new rows over the cache.  workspace: w4_attn_workspace_bytes(...) bytes, zeroed once."""
+    return lib().w4_attn_kv8(cache, _ptr(q), _ptr(out), _ptr(lse), _ptr(q_start), _ptr(kv_len), tokens, batch, q_heads,
+                             max_q, softmax_scale, int(causal), window, q_stride, out_stride, _ptr(workspace),
+                             _nbytes(workspace, workspace_bytes), _stream(stream))
+
+
+def w4_spec_verify_workspace_bytes(batch: int, drafts: int, vocab: int) -> int:
+    return lib().w4_spec_verify_workspace_bytes(batch, drafts, vocab)
+
+
+def w4_spec_verify(target, draft, draft_tokens, u, e, tokens, accepted, logprob, batch, drafts, vocab, temperature,
+                   workspace, n_drafts=None, target_stride=0, draft_stride=0, workspace_bytes=None, stream=None):
+    """Verification of drafted tokens from logits.  workspace: w4_spec_verify_workspace_bytes(...) bytes,
+    zeroed once."""
+    return lib().w4_spec_verify(_ptr(target), _ptr(draft), _ptr(draft_tokens), _ptr(u), _ptr(e), _ptr(tokens),
+                                _ptr(accepted), _ptr(logprob), batch, drafts, vocab, temperature, _ptr(n_drafts),
+                                target_stride, draft_stride, _ptr(workspace), _nbytes(workspace, workspace_bytes),
+                                _stream(stream))

@@ -20,6 +20,10 @@ W4_ERR_CUDA = -5
 W4_ERR_TIMEOUT = -6
 W4_ERR_UNSUPPORTED = -7
 W4_ERR_LIMIT = -8
+W4_ERR_RANGE = -9
+W4_MAX_SEQS = 1024
+W4_MAX_GROUP = 64
+W4_MAX_DRAFTS = 31
 W4_NOALLOC_MAX_LEVELS = 256
 W4_NOALLOC_MAX_GEMVS = 256
 W4_FMT_NF4 = 0
@@ -37,6 +41,7 @@ SYMBOLS = (
     "w4_step_launch", "w4_step_destroy", "w4_status_str", "w4_last_cuda_error", "w4_device_check",
     "w4_launch_count", "w4_inject_timeout_once", "w4_gemv_levels_noalloc", "w4_gemv_plan",
     "w4_quantize_fp4", "w4_dequantize_fp4", "w4_gemv_fp4", "w4_step_run_host",
+    "w4_kv_append", "w4_attn_workspace_bytes", "w4_attn_kv8", "w4_spec_verify_workspace_bytes", "w4_spec_verify",
 )
 
 
@@ -78,11 +83,30 @@ class GemvPlan(ctypes.Structure):
                 ("kernel", "launches", "batch_tile", "threads", "smem_bytes", "stages", "grid", "cluster")]
 
 
+class KvCache(ctypes.Structure):
+    """w4_kv_cache of include/w4.h."""
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64),
+        ("scale_stride", ctypes.c_int64),
+        ("num_pages", ctypes.c_int),
+        ("kv_heads", ctypes.c_int),
+        ("page_tokens", ctypes.c_int),
+        ("head_dim", ctypes.c_int),
+        ("table_stride", ctypes.c_int),
+    ]
+
+
 _lib = None
 
 
 def _declare(L):
     P, I, V = ctypes.c_void_p, ctypes.c_int, None
+    L64, F, C = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(KvCache)
     sig = {
         "w4_nf4_codebook": (I, [P]),
         "w4_quantize_nf4": (I, [P, P, P, P, I, I, I, P]),
@@ -106,6 +130,11 @@ def _declare(L):
         "w4_launch_count": (ctypes.c_longlong, []),
         "w4_inject_timeout_once": (I, []),
         "w4_gemv_levels_noalloc": (I, [ctypes.POINTER(GemvDesc), I, P]),
+        "w4_kv_append": (I, [C, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, L64, L64, L64, L64, P]),
+        "w4_attn_workspace_bytes": (L64, [I, I, I, I, I]),
+        "w4_attn_kv8": (I, [C, P, P, P, P, P, I, I, I, I, F, I, I, L64, L64, P, L64, P]),
+        "w4_spec_verify_workspace_bytes": (L64, [I, I, I]),
+        "w4_spec_verify": (I, [P, P, P, P, P, P, P, P, I, I, I, F, P, L64, L64, P, L64, P]),
         "w4_gemv_plan": (I, [I, I, I, I, I, I, ctypes.POINTER(GemvPlan)]),
     }
     for name, (res, args) in sig.items():

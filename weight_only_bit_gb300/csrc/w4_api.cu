@@ -12,6 +12,7 @@
 
 #include "../../include/w4.h"
 #include "w4_internal.h"
+#include "w4_serve.h"
 
 namespace w4 {
 
@@ -21,17 +22,19 @@ void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 static std::atomic<int> g_inject{0};
 int take_fault_injection() { return g_inject.exchange(0); }
 
-}  // namespace w4
-
-namespace {
-
-thread_local int t_last_cuda_error = 0;
+static thread_local int t_last_cuda_error = 0;
 
 int cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return W4_OK;
   t_last_cuda_error = static_cast<int>(e);
   return W4_ERR_CUDA;
 }
+
+}  // namespace w4
+
+namespace {
+
+using w4::cuda_status;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -488,21 +491,29 @@ const char* w4_status_str(int status) {
     case W4_ERR_CUDA: return "CUDA runtime error";
     case W4_ERR_TIMEOUT: return "device-side wait timed out";
     case W4_ERR_UNSUPPORTED: return "unsupported by this build";
+    case W4_ERR_RANGE: return "a page id or position held on the device is out of range";
     case W4_ERR_LIMIT: return "beyond the fixed counter array of w4_gemv_levels_noalloc (256 levels, 256 GEMVs)";
     default: return "unknown status";
   }
 }
 
-int w4_last_cuda_error(void) { return t_last_cuda_error; }
+int w4_last_cuda_error(void) { return w4::t_last_cuda_error; }
 
 int w4_device_check(w4_stream_t stream) {
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_status(e);
-  // every translation unit's copy of the error word: the small-batch and the tensor-core kernels
-  const unsigned int v = w4::read_clear_error_persist() | w4::read_clear_error_tc5();
+  // every translation unit's copy of the error word: the small-batch and the tensor-core GEMV kernels,
+  // the cache append and the attention
+  const unsigned int words[] = {w4::read_clear_error_persist(), w4::read_clear_error_tc5(), w4::read_clear_error_kv(),
+                                w4::read_clear_error_attn()};
+  bool lost = false, range = false;
+  for (unsigned int w : words) {
+    if (w & w4::kRangeBit) range = true;
+    else if (w) lost = true;
+  }
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_status(e);
-  return v ? W4_ERR_TIMEOUT : W4_OK;
+  return lost ? W4_ERR_TIMEOUT : range ? W4_ERR_RANGE : W4_OK;
 }
 
 long long w4_launch_count(void) { return w4::g_launches.load(); }

@@ -70,6 +70,14 @@ int device_sm_count();
 bool encode_tmap_2d(CUtensorMap* m, int es, const void* base, long long cols, long long rows, int box_cols,
                     int box_rows);
 
+// 3-D tiled TMA map over a paged cache of 1-byte codes, [pages][rows][dim] with `page_stride` bytes from a
+// page to the next: box of one page's box_rows x dim, swizzled over the whole row (128 or 64 bytes).
+bool encode_tmap_pages(CUtensorMap* m, const void* base, int dim, long long rows, long long pages, long long page_stride,
+                       int box_rows);
+
+// Keeps the error for w4_last_cuda_error() and returns the w4_status that stands for it.
+int cuda_status(cudaError_t e);
+
 // Unique id of the CUDA context current on this thread (the runtime's primary context of the current
 // device; a new id after cudaDeviceReset), or 0 if the driver cannot say.
 unsigned long long current_context_id();

@@ -1,0 +1,339 @@
+// w4_kv.cu -- rotation of new q and k rows by their positions and the append of k and v to a paged
+// 8-bit cache (sm_103a).
+//
+// Mathematics.  Rotation: each pair (a, b) of channels turns by the angle pos * freq_j, in FP32 with the
+// products and the sum rounded one by one (no contraction).  A block (page x head, K or V) holds E4M3
+// codes under one power-of-two scale s, the smallest with amax <= 448 s: dividing by s is exact, so a
+// value is rounded once, to E4M3's 4 significant bits, and when a later token of the page needs a
+// larger s the codes that are there move by whole binades: only those that fall below E4M3's normal
+// range (2^-6 s) lose bits.  A power of two costs up to one binade of that range and no precision.
+//
+// Work split.  One CTA per (sequence, touched page, kv head) does K and V of the new rows in the page:
+// it needs both, because a NaN in a token's v marks the token's key.  It reads the rows twice, once
+// for amax and once to write the codes (the second read comes from L1): a page of 64 rows is 16 KB of
+// each, too much for registers at a useful occupancy.  Rows of q need no such unit: a warp per row.
+// What bounds it: DRAM bytes for prompts (q read and written, k and v read, codes written), launch
+// latency for single tokens.
+#include <cstdint>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "w4_common.cuh"
+#include "w4_internal.h"
+#include "w4_serve.h"
+
+namespace w4 {
+
+constexpr int kKvThreads = 128;
+
+__device__ __forceinline__ void kv_range_error(uint32_t site) { atomicCAS(&g_error_word, 0u, kRangeBit | site); }
+
+struct Rot {
+  float c[8], s[8];
+};
+
+__device__ __forceinline__ void load8(const __half* p, float (&x)[8]) {
+  const uint4 w = ld_nc_v4(p);
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+__device__ __forceinline__ void load_rot(const AppendArgs& a, int pos, int lane, Rot& r) {
+  const size_t o = (size_t)pos * (a.rotary_dim / 2) + 8 * lane;
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) {
+    const float4 c = __ldg(reinterpret_cast<const float4*>(a.cos + o + i));
+    const float4 s = __ldg(reinterpret_cast<const float4*>(a.sin + o + i));
+    r.c[i] = c.x; r.c[i + 1] = c.y; r.c[i + 2] = c.z; r.c[i + 3] = c.w;
+    r.s[i] = s.x; r.s[i + 1] = s.y; r.s[i + 2] = s.z; r.s[i + 3] = s.w;
+  }
+}
+
+// Lane l of a row's D / 16 lanes owns two chunks of 8 channels.  Rotated lanes (l < R / 16): chunks
+// l and l + R / 16 (halves) or 2l and 2l + 1 (interleaved), both with the angles 8l ... 8l + 7.  The
+// other lanes: two neighbouring chunks above R, unchanged.
+struct Chunks {
+  int c0, c1;
+  bool rot;
+};
+__device__ __forceinline__ Chunks chunks_of(int l, int rotary_dim, int interleaved) {
+  const int rl = rotary_dim >> 4;
+  Chunks k;
+  k.rot = l < rl;
+  if (k.rot && !interleaved) {
+    k.c0 = l;
+    k.c1 = l + rl;
+  } else {
+    k.c0 = 2 * l;                  // above R: R / 8 + 2 (l - R / 16) = 2l
+    k.c1 = 2 * l + 1;
+  }
+  return k;
+}
+
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+  const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  const float y = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  a = x;
+  b = y;
+}
+
+__device__ __forceinline__ void rotate(float (&x0)[8], float (&x1)[8], const Rot& r, int interleaved) {
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      turn(x0[2 * i], x0[2 * i + 1], r.c[i], r.s[i]);
+      turn(x1[2 * i], x1[2 * i + 1], r.c[4 + i], r.s[4 + i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turn(x0[i], x1[i], r.c[i], r.s[i]);
+  }
+}
+
+// The smallest power of two s with amax <= 448 s = 1.75 * 2^8 s, at least 2^-60 (amax finite, >= 0).
+__device__ __forceinline__ float power_scale(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  int e = (int)(u >> 23) - ((u & 0x7fffffu) <= 0x600000u ? 8 : 7);   // mantissa <= 1.75
+  e = max(e, 127 - 60);
+  return __uint_as_float((uint32_t)e << 23);
+}
+
+// Two FP32 values to E4M3 codes, nearest even, saturating (first value in the low byte).
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float s) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], s);
+  return make_uint2(e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16, e4m3x2(y[4], y[5]) | e4m3x2(y[6], y[7]) << 16);
+}
+
+// Four E4M3 codes times `f`, rounded to E4M3 again.
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
+  uint32_t h[2];
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(h[0]), "=r"(h[1]) : "r"(w));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[0]));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h[1]));
+  return e4m3x2(__fmul_rn(a.x, f), __fmul_rn(a.y, f)) | e4m3x2(__fmul_rn(b.x, f), __fmul_rn(b.y, f)) << 16;
+}
+
+// Sequence of row t (q_start[b] <= t < q_start[b + 1]), by the whole warp: 32 probes a round.
+__device__ __forceinline__ int find_seq(const int32_t* q_start, int batch, int t, int lane) {
+  int lo = 0, n = batch;                      // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int i = lo + lane * step;
+    const bool le = lane * step < n && __ldg(q_start + i) <= t;
+    const int k = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
+    n = min(step, n - k * step);
+    lo += k * step;
+  }
+  return lo;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kKvThreads) w4_kv_append_kernel(const __grid_constant__ AppendArgs a, int upb) {
+  constexpr int LPR = D / 16;                 // lanes per row
+  constexpr int RPP = kKvThreads / LPR;       // rows per pass
+  __shared__ float red[kKvThreads / 32][2];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int l = tid % LPR;
+  const Chunks ck = chunks_of(l, a.rotary_dim, a.interleaved);
+  const int nkv = a.batch * upb * a.c.kv_heads;
+  if ((int)blockIdx.x >= nkv) {
+    // ------------------------------------------------ q rows: a warp per row
+    const int t = ((int)blockIdx.x - nkv) * (kKvThreads / 32) + warp;
+    if (t >= a.tokens) return;
+    const int b = find_seq(a.q_start, a.batch, t, lane);
+    const int p = __ldg(a.kv_len + b) - __ldg(a.q_start + b + 1) + t;
+    int pos = p;
+    bool ok = p >= 0;
+    if (ok && a.rotary_dim > 0) {
+      if (a.positions) pos = __ldg(a.positions + t);
+      if (pos < 0 || pos >= a.max_position) {
+        ok = false;
+        if (lane == 0) kv_range_error(0x401);
+      }
+    }
+    Rot r;
+    const bool rot = ck.rot && ok;
+    if (rot) load_rot(a, pos, l, r);
+    for (int h = lane / LPR; h < a.q_heads; h += 32 / LPR) {
+      const __half* src = a.q + (long long)t * a.q_stride + (long long)h * D;
+      __half* dst = a.q_out + (long long)t * a.q_out_stride + (long long)h * D;
+      float x0[8], x1[8];
+      load8(src + 8 * ck.c0, x0);
+      load8(src + 8 * ck.c1, x1);
+      if (rot) rotate(x0, x1, r, a.interleaved);
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 u = __floats2half2_rn(x0[2 * i], x0[2 * i + 1]), v = __floats2half2_rn(x1[2 * i], x1[2 * i + 1]);
+        w[i] = ok ? *reinterpret_cast<const uint32_t*>(&u) : 0u;
+        w[4 + i] = ok ? *reinterpret_cast<const uint32_t*>(&v) : 0u;
+      }
+      *reinterpret_cast<uint4*>(dst + 8 * ck.c0) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(dst + 8 * ck.c1) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    return;
+  }
+  // -------------------------------------------------- one page of one sequence, one kv head
+  const int h = (int)blockIdx.x % a.c.kv_heads;
+  const int u = (int)blockIdx.x / a.c.kv_heads;
+  const int b = u / upb;
+  const int start = __ldg(a.q_start + b), n = __ldg(a.q_start + b + 1) - start;
+  const int total = __ldg(a.kv_len + b);
+  const int P = a.c.page;
+  if (start < 0 || start + n > a.tokens || n > a.max_q) {   // not what the caller said of q_start
+    if (tid == 0) kv_range_error(0x404);
+    return;
+  }
+  const int old = max(total - n, 0);               // tokens that were in the cache
+  const int pg = old / P + u % upb;
+  if (n <= 0 || (long long)pg * P >= total) return;
+  const int r0 = max(old - pg * P, 0);             // the page's rows [r0, r1) are new
+  const int r1 = min(total - pg * P, P);
+  const int id = pg < a.c.table_stride ? __ldg(a.c.table + (long long)b * a.c.table_stride + pg) : -1;
+  if (id < 0 || id >= a.c.num_pages) {
+    if (tid == 0) kv_range_error(0x402);
+    return;
+  }
+  const int t0 = start + pg * P - (total - n);      // row of q, k, v of the page's row 0
+  uint8_t* kb = a.c.k + (long long)id * a.c.page_stride + (long long)h * P * D;
+  uint8_t* vb = a.c.v + (long long)id * a.c.page_stride + (long long)h * P * D;
+  // one row's 16 k and 16 v values of this lane, k rotated; nan: a NaN among the row's values
+  auto fetch = [&](int row, float (&k0)[8], float (&k1)[8], float (&v0)[8], float (&v1)[8]) -> bool {
+    const int t = t0 + row;
+    const __half* ks = a.k + (long long)t * a.k_stride + (long long)h * D;
+    const __half* vs = a.v + (long long)t * a.v_stride + (long long)h * D;
+    load8(ks + 8 * ck.c0, k0);
+    load8(ks + 8 * ck.c1, k1);
+    load8(vs + 16 * l, v0);
+    load8(vs + 16 * l + 8, v1);
+    if (a.rotary_dim > 0) {
+      const int pos = a.positions ? __ldg(a.positions + t) : pg * P + row;
+      if (pos < 0 || pos >= a.max_position) return false;
+      if (ck.rot) {
+        Rot r;
+        load_rot(a, pos, l, r);
+        rotate(k0, k1, r, a.interleaved);
+      }
+    }
+    return true;
+  };
+  auto finite_abs = [](float x) { return fabsf(x) <= 3.402823466e38f ? fabsf(x) : 0.f; };
+  float ak = 0.f, av = 0.f;
+  for (int row = r0 + tid / LPR; row < r1; row += RPP) {
+    float k0[8], k1[8], v0[8], v1[8];
+    if (!fetch(row, k0, k1, v0, v1)) {
+      kv_range_error(0x403);
+      continue;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      ak = fmaxf(ak, fmaxf(finite_abs(k0[i]), finite_abs(k1[i])));
+      av = fmaxf(av, fmaxf(finite_abs(v0[i]), finite_abs(v1[i])));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    ak = fmaxf(ak, __shfl_xor_sync(0xffffffffu, ak, o));
+    av = fmaxf(av, __shfl_xor_sync(0xffffffffu, av, o));
+  }
+  if (lane == 0) {
+    red[warp][0] = ak;
+    red[warp][1] = av;
+  }
+  float* ksp = a.c.k_scale + (long long)id * a.c.scale_stride + h;
+  float* vsp = a.c.v_scale + (long long)id * a.c.scale_stride + h;
+  const float ok = r0 > 0 ? *ksp : 0.f, ov = r0 > 0 ? *vsp : 0.f;   // scales of the rows that are there
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kKvThreads / 32; ++w) {
+    ak = fmaxf(ak, red[w][0]);
+    av = fmaxf(av, red[w][1]);
+  }
+  const float sk = fmaxf(ok, power_scale(ak)), sv = fmaxf(ov, power_scale(av));
+  if (tid == 0) {
+    *ksp = sk;
+    *vsp = sv;
+  }
+  // rows that share the page go over to a scale that grew
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const float so = m ? ov : ok, sn = m ? sv : sk;
+    if (r0 > 0 && so > 0.f && sn > so) {
+      const float f = __fdiv_rn(so, sn);
+      uint4* base = reinterpret_cast<uint4*>(m ? vb : kb);
+      for (int i = tid; i < r0 * (D / 16); i += kKvThreads) {
+        uint4 w = base[i];
+        w.x = rescale4(w.x, f);
+        w.y = rescale4(w.y, f);
+        w.z = rescale4(w.z, f);
+        w.w = rescale4(w.w, f);
+        base[i] = w;
+      }
+    }
+  }
+  // the new rows (all lanes of a warp go round together: the row's lanes vote on NaNs)
+  for (int r = r0; r < r1; r += RPP) {
+    const int row = r + tid / LPR;
+    float k0[8], k1[8], v0[8], v1[8];
+    const bool live = row < r1 && fetch(row, k0, k1, v0, v1);
+    bool nan = false;
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        nan |= k0[i] != k0[i] || k1[i] != k1[i] || v0[i] != v0[i] || v1[i] != v1[i];
+        if (v0[i] != v0[i]) v0[i] = 0.f;
+        if (v1[i] != v1[i]) v1[i] = 0.f;
+      }
+    }
+    const uint32_t mask = __ballot_sync(0xffffffffu, nan);
+    if (!live) continue;
+    uint2 c0 = codes8(k0, sk), c1 = codes8(k1, sk);
+    const uint32_t mine = ((1u << LPR) - 1u) << (lane / LPR * LPR);
+    if (mask & mine) c0 = c1 = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+    const uint2 d0 = codes8(v0, sv), d1 = codes8(v1, sv);
+    *reinterpret_cast<uint2*>(kb + (long long)row * D + 8 * ck.c0) = c0;
+    *reinterpret_cast<uint2*>(kb + (long long)row * D + 8 * ck.c1) = c1;
+    *reinterpret_cast<uint4*>(vb + (long long)row * D + 16 * l) = make_uint4(d0.x, d0.y, d1.x, d1.y);
+  }
+}
+
+cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
+  // pages that a sequence's new rows can touch: its first may be partly filled
+  const int upb = (a.max_q + a.c.page - 2) / a.c.page + 1;
+  const long long nkv = (long long)a.batch * upb * a.c.kv_heads;
+  const long long nq = a.q ? (a.tokens + kKvThreads / 32 - 1) / (kKvThreads / 32) : 0;
+  if (nkv + nq > 0x7fffffffLL) return cudaErrorNotSupported;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(nkv + nq));
+  cfg.blockDim = dim3(kKvThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = a.c.dim == 128 ? cudaLaunchKernelEx(&cfg, w4_kv_append_kernel<128>, a, upb)
+                                       : cudaLaunchKernelEx(&cfg, w4_kv_append_kernel<64>, a, upb);
+  note_launch();
+  return e;
+}
+
+unsigned int read_clear_error_kv() { return read_clear_error_word_here(); }
+
+}  // namespace w4

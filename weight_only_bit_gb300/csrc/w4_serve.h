@@ -1,0 +1,72 @@
+// w4_serve.h -- host-side declarations of the cache, attention and verification kernels (not
+// installed).
+#pragma once
+#include <cstdint>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/w4.h"
+
+namespace w4 {
+
+// A device error word with this bit set reports an index out of range (W4_ERR_RANGE), without it a
+// lost wait (W4_ERR_TIMEOUT).
+constexpr unsigned int kRangeBit = 0x80000000u;
+
+// The cache as the kernels take it: strides filled in.
+struct KvView {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* table;
+  long long page_stride, scale_stride;
+  int num_pages, kv_heads, page, dim, table_stride;
+};
+
+struct AppendArgs {
+  KvView c;
+  const __half *q, *k, *v;
+  __half* q_out;
+  const float *cos, *sin;
+  const int32_t *positions, *q_start, *kv_len;
+  int tokens, batch, q_heads, max_q, max_position, rotary_dim, interleaved;
+  long long q_stride, k_stride, v_stride, q_out_stride;
+};
+cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
+
+struct AttnArgs {
+  KvView c;
+  const __half* q;
+  __half* out;
+  float* lse;
+  const int32_t *q_start, *kv_len;
+  int tokens, batch, q_heads, max_q;
+  float scale;
+  int causal, window;
+  long long q_stride, out_stride;
+  void* workspace;
+};
+int64_t attn_workspace_bytes(int tokens, int batch, int q_heads, int kv_heads, int head_dim);
+cudaError_t launch_attn(const AttnArgs& a, cudaStream_t stream);
+
+struct VerifyArgs {
+  const __half *target, *draft;
+  const int32_t* draft_tokens;
+  const float *u, *e;
+  int32_t *tokens, *accepted;
+  float* logprob;
+  int batch, drafts, vocab;
+  float temperature;
+  const int32_t* n_drafts;
+  long long target_stride, draft_stride;
+  void* workspace;
+};
+int64_t verify_workspace_bytes(int batch, int drafts, int vocab);
+cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream);
+
+// Each translation unit's device error word, read and cleared on the current device.
+unsigned int read_clear_error_kv();
+unsigned int read_clear_error_attn();
+
+}  // namespace w4

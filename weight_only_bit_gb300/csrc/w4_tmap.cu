@@ -65,4 +65,17 @@ bool encode_tmap_2d(CUtensorMap* m, int es, const void* base, long long cols, lo
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tmap_pages(CUtensorMap* m, const void* base, int dim, long long rows, long long pages, long long page_stride,
+                       int box_rows) {
+  EncodeFn enc = encoder();
+  if (!enc || (dim != 64 && dim != 128)) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)rows, (cuuint64_t)pages};
+  const cuuint64_t strides[2] = {(cuuint64_t)dim, (cuuint64_t)page_stride};
+  const cuuint32_t box[3] = {(cuuint32_t)dim, (cuuint32_t)box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace w4
