@@ -344,7 +344,7 @@ int w4_kv_append(const w4_kv_cache* cache, const uint16_t* q, const uint16_t* k,
  * and the output are FP32, weights are rounded to FP16 for the product with V, out to FP16.
  * One launch for every mix of lengths; the split over the keys is decided on the device from
  * q_start and kv_len, and the pieces are joined in a fixed order (repeated calls give the same
- * bits).  max_q: at least the largest n_b.  workspace: w4_attn_workspace_bytes(...) bytes of device
+ * bits).  softmax_scale > 0.  max_q: at least the largest n_b.  workspace: w4_attn_workspace_bytes(...) bytes of device
  * memory, 16-byte aligned, zeroed by the caller before its first use and left ready for the next call
  * by each call; calls that overlap on the GPU need one each.  q, out 16-byte aligned, strides
  * multiples of 8 elements, page_stride a multiple of 16 bytes.  A page id outside [0, num_pages)

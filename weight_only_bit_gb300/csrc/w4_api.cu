@@ -505,7 +505,7 @@ int w4_device_check(w4_stream_t stream) {
   // every translation unit's copy of the error word: the small-batch and the tensor-core GEMV kernels,
   // the cache append and the attention
   const unsigned int words[] = {w4::read_clear_error_persist(), w4::read_clear_error_tc5(), w4::read_clear_error_kv(),
-                                w4::read_clear_error_attn()};
+                                w4::read_clear_error_attn(), w4::read_clear_error_attn5()};
   bool lost = false, range = false;
   for (unsigned int w : words) {
     if (w & w4::kRangeBit) range = true;

@@ -1,0 +1,635 @@
+// w4_attn5.cu -- attention of new rows over a paged 8-bit cache on the 5th-generation tensor cores
+// (tcgen05), for prompts, chunks and everything with more rows per sequence and kv head than w4_attn.cu
+// takes (sm_103a).
+//
+// Mathematics: as in w4_attn.cu (the page scale of V rides in the exponent, the bound on the logits
+// moves only when one passes it by kA5Slack).  With 128 rows and more, a decoded key serves enough
+// products that the work is a dense contraction: S = Q K^T and O += P V, both M = 128, FP16 x FP16 ->
+// FP32 with the accumulators in tensor memory.
+//
+// An item has up to 256 rows: two row tiles of 128, each with its own S, O and softmax warpgroup
+// ("streams").  An item of at most 128 rows gives both streams the same rows and every second key
+// tile each, joined at the end; so the two softmax warpgroups always overlap the other's products.
+// Tensor memory is full: S 2 x 128 columns, O 2 x D columns (256 at D = 128); the weights P go back
+// over the first half of their S as FP16, the A operand of the second product.
+// Roles (17 warps), connected by mbarriers:
+//   warps 0-3, 4-7   softmax of stream 0 and 1: a thread per row.  Load Q, then per key tile: maximum,
+//                    weights, sums, P; O is rescaled in place when the bound moved; at the end out.
+//   warps 8-11       keys: codes from global memory, FP16 into the canonical K-major layout
+//   warps 12-15      values: the same into the MN-major layout (channels contiguous, as they lie in
+//                    memory: nothing is transposed)
+//   warp 16          issues the MMAs: PV of a stream, then its next S, alternating between streams
+// What bounds it: figures beside the launch below.
+#include <cstdint>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "w4_attn.cuh"
+#include "w4_common.cuh"
+#include "w4_internal.h"
+#include "w4_serve.h"
+#include "w4_t5.cuh"
+
+namespace w4 {
+
+constexpr int kA5T = 128;                    // keys per tile
+constexpr int kA5R = 256;                    // rows per item
+constexpr int kA5Threads = 17 * 32;
+constexpr float kA5Slack = 6.f;
+constexpr int kA5ScaleSlots = 4;
+
+template <int D>
+struct A5Smem {
+  static constexpr int kTile = 128 * D * 2;              // 128 rows of FP16: D / 64 blocks of 128 x 128 bytes
+  static constexpr int oQ = 0;                           // two streams
+  static constexpr int oK = 2 * kTile;                   // two stages
+  static constexpr int oV = 4 * kTile;
+  static constexpr int oScales = 6 * kTile;              // [slots][8 groups] (ks c, log2 vs, 1 / vs, 0)
+  static constexpr int oMl = oScales + kA5ScaleSlots * 8 * 16;   // [128] (maximum, sum) of stream 1
+  static constexpr int oBar = oMl + 128 * 8;
+  static constexpr int kBars = 2 + 2 + 2 + 2 + kA5ScaleSlots + 2 + 2 + 2 + 2 + 1;
+  static constexpr int oFlag = oBar + kBars * 8;
+  static constexpr int oPrefix = oFlag + 16;
+  static constexpr int kTotal = oPrefix + (W4_MAX_SEQS + 1) * 4 + 1024;
+};
+
+struct A5Params {
+  AttnArgs a;
+  int group, max_blocks, min_units;
+};
+
+// Shared-memory matrix descriptors (version 1, 128-byte swizzle).  K-major: rows of 128 bytes, 8-row
+// groups 1024 bytes apart (stride offset); a K = 16 step moves the start by 32 bytes.
+__device__ __forceinline__ uint64_t a5_desc_k(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// MN-major: rows (one per key) of 64 channels = 128 bytes, 8-key groups 1024 bytes apart (stride
+// offset), the next 64 channels 16 KB on (leading offset); a K = 16 step moves the start by 2048 bytes.
+__device__ __forceinline__ uint64_t a5_desc_mn(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(16384 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
+         (2ull << 61);
+}
+// kind::f16, FP32 D, FP16 A and B, M = 128, N; bit 16: B is MN-major.
+__host__ __device__ constexpr uint32_t a5_idesc(int N, bool mn) {
+  return (1u << 4) | (mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+
+__device__ __forceinline__ void a5_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void a5_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+}
+__device__ __forceinline__ void a5_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t a5_pack(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 16 codes to 16 FP16 values.
+__device__ __forceinline__ void a5_cvt16(uint4 w, uint4& lo, uint4& hi) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+        : "=r"(o[2 * i]), "=r"(o[2 * i + 1]) : "r"(in[i]));
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+__device__ __forceinline__ void a5_sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ float4 a5_lds_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+// Generic shared-memory writes before, tensor-core reads after.
+__device__ __forceinline__ void a5_fence_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void a5_sync_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void a5_sync_stream(int s) { asm volatile("bar.sync %0, 128;" ::"r"(2 + s) : "memory"); }
+
+template <int D>
+__global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_constant__ A5Params p) {
+  using S = A5Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sb = smem_u32(smem);
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + S::oBar);   // 4 key warps
+  uint64_t* kempty = kfull + 2;                                   // commit
+  uint64_t* vfull = kempty + 2;
+  uint64_t* vempty = vfull + 2;
+  uint64_t* scfull = vempty + 2;                                  // 4 key warps
+  uint64_t* sfull = scfull + kA5ScaleSlots;                       // commit: S of the stream is there
+  uint64_t* pfull = sfull + 2;                                    // 4 softmax warps: P of the stream is there
+  uint64_t* qfull = pfull + 2;                                    // 4 softmax warps: Q of the stream is there
+  uint64_t* ofull = qfull + 2;                                    // commit: O of the stream is complete
+  uint64_t* done = ofull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::oFlag);
+  int* flag = reinterpret_cast<int*>(smem + S::oFlag + 8);
+  int* bad = flag + 1;                       // a softmax warp lost a wait: all of them leave together
+  int* prefix = reinterpret_cast<int*>(smem + S::oPrefix);
+  const AttnArgs& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&kfull[i], 4);
+      mbar_init(&kempty[i], 1);
+      mbar_init(&vfull[i], 4);
+      mbar_init(&vempty[i], 1);
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], 4);
+      mbar_init(&qfull[i], 4);
+      mbar_init(&ofull[i], 1);
+    }
+    for (int i = 0; i < kA5ScaleSlots; ++i) mbar_init(&scfull[i], 4);
+    mbar_init(done, 1);
+    *bad = 0;
+    fence_mbar_init();
+  }
+  if (warp == 16) t5_alloc512(tmem_slot);
+  t5_fence_before();
+  __syncthreads();
+  t5_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+  const Split sp = attn_split<kA5R, kA5T>(a, p.group, p.max_blocks, p.min_units, (int)gridDim.x, prefix);
+  const int cta = (int)blockIdx.x;
+  const int begin = cta < sp.ctas && sp.U > 0 ? sp.first(cta) : 0, end = cta < sp.ctas && sp.U > 0 ? sp.first(cta + 1) : 0;
+  bool ok = true;
+  if (begin < end) {
+    Walk<kA5R, kA5T> w;
+    w.start(a, p.group, prefix, begin, end);
+    const float c2 = a.scale * 1.4426950408889634f;
+    if (warp >= 8 && warp < 16) {
+      // ================================================================ keys or values into shared memory
+      const bool is_v = warp >= 12;
+      const int wq = warp & 3;                       // rows 32 wq ... + 31 of the tile
+      constexpr int LPR = D / 16;                    // lanes per row
+      constexpr int RPI = 32 / LPR;                  // rows per pass of the warp
+      constexpr int NP = 32 / RPI;                   // passes
+      const int l = lane % LPR, rl = lane / LPR;
+      const uint8_t* pool = is_v ? a.c.v : a.c.k;
+      uint64_t* full = is_v ? vfull : kfull;
+      uint64_t* empty = is_v ? vempty : kempty;
+      const uint32_t base = sb + (is_v ? S::oV : S::oK);
+      const int P = a.c.page;
+      int u = w.u0, j = 0;
+      bool more = true;
+      // lane g < 2: page of the warp's 16-key group g of the tile
+      auto pages_of = [&](bool have) {
+        int page = -1;
+        if (have && lane < 2) {
+          const int key = (w.it.t0 + u) * kA5T + wq * 32 + lane * 16;
+          if (key < w.it.hi && key + 16 > w.it.lo) {
+            page = __ldg(a.c.table + (long long)w.it.b * a.c.table_stride + key / P);
+            if (page < 0 || page >= a.c.num_pages) {
+              attn_range_error(0x502);
+              page = -1;
+            }
+          }
+        }
+        return page;
+      };
+      uint4 data[NP];
+      float4 sc = make_float4(0.f, 0.f, 1.f, 0.f);
+      // issues the loads of the tile at (w, u); its scales too (key warps)
+      auto load = [&](int page) {
+        const int k0 = (w.it.t0 + u) * kA5T + wq * 32;
+        const int pg0 = __shfl_sync(0xffffffffu, page, 0), pg1 = __shfl_sync(0xffffffffu, page, 1);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const int r = i * RPI + rl;
+          const int key = k0 + r;
+          const int pg = r < 16 ? pg0 : pg1;
+          // rows that nobody sees are zero: their weights are 0, and 0 times a stale NaN would not be
+          data[i] = make_uint4(0, 0, 0, 0);
+          if (pg >= 0 && key >= w.it.lo && key < w.it.hi)
+            data[i] = ld_nc_v4(pool + (long long)pg * a.c.page_stride + (long long)(w.it.h * P + key % P) * D + 16 * l);
+        }
+        if (!is_v) {
+          sc = make_float4(0.f, 0.f, 1.f, 0.f);
+          if (lane < 2 && page >= 0) {
+            sc.x = __ldg(a.c.k_scale + (long long)page * a.c.scale_stride + w.it.h) * c2;
+            const float vs = __ldg(a.c.v_scale + (long long)page * a.c.scale_stride + w.it.h);
+            sc.y = log2f(vs);
+            sc.z = __fdiv_rn(1.f, vs);
+          }
+        }
+      };
+      load(pages_of(true));
+      while (more && ok) {
+        // the next tile's pages, while this one's data are on their way
+        if (++u >= w.u1) {
+          more = w.next(a, p.group);
+          u = w.u0;
+        }
+        const int page = pages_of(more);
+        const int st = j & 1;
+        if (j >= 2) ok = mbar_wait(&empty[st], ((j >> 1) - 1) & 1, is_v ? 0x521 : 0x522);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t dst = base + st * S::kTile + ((16 * l) / 64) * 16384;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const int r = wq * 32 + i * RPI + rl;
+          uint4 x[2];
+          a5_cvt16(data[i], x[0], x[1]);
+          // 16-byte chunks 2 (l % 4) and the next of the row's 128 bytes; half of the lanes begin with
+          // the second, so that a quarter-warp's stores meet all banks once
+          const int first = (l >> 2) & 1;
+          const uint32_t row = dst + r * 128;
+          const int c = 2 * (l & 3);
+          a5_sts128(row + (((c + first) ^ (r & 7)) << 4), x[first]);
+          a5_sts128(row + (((c + 1 - first) ^ (r & 7)) << 4), x[1 - first]);
+        }
+        if (!is_v && lane < 2)
+          *reinterpret_cast<float4*>(smem + S::oScales + ((j & (kA5ScaleSlots - 1)) * 8 + wq * 2 + lane) * 16) = sc;
+        a5_fence_proxy();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&full[st]);
+          if (!is_v) mbar_arrive(&scfull[j & (kA5ScaleSlots - 1)]);
+        }
+        ++j;
+        if (more) load(page);
+      }
+    } else if (warp == 16) {
+      // ================================================================ MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t id_s = a5_idesc(128, false), id_o = a5_idesc(D, true);
+        int tb = 0, items = 0;                       // tiles and items before this one
+        int jobs[2] = {0, 0};                        // jobs of each stream so far
+        bool more = true;
+        while (more && ok) {
+          const int n = w.u1 - w.u0;
+          const bool two = w.it.n * p.group - w.it.rb * kA5R > 128;
+          const int nq = two ? 2 * n : n;
+          ok = mbar_wait(&qfull[0], items & 1, 0x523) && mbar_wait(&qfull[1], items & 1, 0x524);
+          auto qk = [&](int q) {
+            const int s = q & 1, tile = tb + (two ? q >> 1 : q);
+            if (!two || s == 0) ok = ok && mbar_wait(&kfull[tile & 1], (tile >> 1) & 1, 0x525);
+            if (!ok) return;
+            t5_fence_after();
+            const uint32_t qa = sb + S::oQ + s * S::kTile, ka = sb + S::oK + (tile & 1) * S::kTile;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+              t5_mma_ss(tmem + s * 128, a5_desc_k(qa + off), a5_desc_k(ka + off), id_s, k > 0 ? 1u : 0u);
+            }
+            t5_commit(&sfull[s]);
+            if (!two || s == 1) t5_commit(&kempty[tile & 1]);
+          };
+          auto pv = [&](int q) {
+            const int s = q & 1, tile = tb + (two ? q >> 1 : q);
+            if (!two || s == 0) ok = ok && mbar_wait(&vfull[tile & 1], (tile >> 1) & 1, 0x526);
+            ok = ok && mbar_wait(&pfull[s], jobs[s] & 1, 0x527);
+            if (!ok) return;
+            ++jobs[s];
+            t5_fence_after();
+            const uint32_t va = sb + S::oV + (tile & 1) * S::kTile;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              t5_mma_ts(tmem + 256 + s * D, tmem + s * 128 + k * 8, a5_desc_mn(va + k * 2048), id_o, (q >= 2 || k > 0) ? 1u : 0u);
+            if (!two || s == 1) t5_commit(&vempty[tile & 1]);
+            if (q + 2 >= nq) t5_commit(&ofull[s]);
+          };
+          if (ok) qk(0);
+          if (ok && nq > 1) qk(1);
+          if (ok && nq == 1) t5_commit(&ofull[1]);   // the other stream has no tile
+          for (int q = 0; q < nq && ok; ++q) {
+            pv(q);
+            if (ok && q + 2 < nq) qk(q + 2);
+          }
+          tb += n;
+          ++items;
+          more = w.next(a, p.group);
+        }
+        t5_commit(done);                             // nothing in flight when tensor memory is freed
+        mbar_wait(done, 0, 0x528);
+      }
+      __syncwarp();
+    } else if (warp < 8) {
+      // ================================================================ softmax
+      const int s = warp >> 2;
+      const int tr = tid & 127;                      // row of the stream's tile = tensor-memory lane
+      const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      const uint32_t ts = tl + s * 128, to = tl + 256 + s * D;
+      const uint32_t sq = sb + S::oQ + s * S::kTile;
+      int jt = 0, items = 0, jobs = 0;
+      bool more = true;
+      while (more) {
+        const Item& it = w.it;
+        const int rows = it.n * p.group - it.rb * kA5R;          // of the item, maybe above 256
+        const bool two = rows > 128;
+        const int off = two ? s * 128 : 0;                       // first row of this stream in the item
+        const int n = w.u1 - w.u0;
+        const int shift = it.total - it.n;
+        // ---- Q: 16-byte chunks, rows beyond the item zero
+        for (int e = tr; e < 128 * (D / 8); e += 128) {
+          const int r = e / (D / 8), ch = e % (D / 8);
+          const int gr = it.rb * kA5R + off + r;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (off + r < rows)
+            v = ld_nc_v4(a.q + (long long)(it.start + gr / p.group) * a.q_stride + (long long)(it.h * p.group + gr % p.group) * D + 8 * ch);
+          a5_sts128(sq + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4), v);
+        }
+        a5_fence_proxy();
+        t5_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qfull[s]);
+        const int gr = it.rb * kA5R + off + tr;
+        const bool valid = off + tr < rows;
+        const int pos = shift + gr / p.group;
+        // keys [rlo, rhi) that this row sees (rows beyond the item see all, and are not stored)
+        const int rhi = !valid ? 0x7fffffff : pos < 0 ? 0 : a.causal ? min(it.total, pos + 1) : it.total;
+        const int rlo = !valid ? 0 : a.window > 0 ? pos - a.window + 1 : 0;
+        float m = -INFINITY, l = 0.f;
+        const int nj = two ? n : (n - s + 1) / 2;
+        for (int q = 0; q < nj; ++q, ++jobs) {
+          const int tile = two ? q : 2 * q + s;
+          const int slot = (jt + tile) & (kA5ScaleSlots - 1);
+          if (ok) ok = mbar_wait(&scfull[slot], ((jt + tile) / kA5ScaleSlots) & 1, 0x529);
+          if (ok) ok = mbar_wait(&sfull[s], jobs & 1, 0x52a);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          t5_fence_after();
+          const int k0 = (it.t0 + w.u0 + tile) * kA5T;
+          const uint32_t ssc = sb + S::oScales + slot * 128;
+          const int clo = rlo - k0, chi = rhi - k0;              // columns that the row sees
+          const bool masked = __any_sync(0xffffffffu, clo > 0 || chi < kA5T);
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            a5_ld32(ts + c * 32, v);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float4 sc = a5_lds_f4(ssc + (c * 2 + h) * 16);
+              float x = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int col = c * 32 + h * 16 + i;
+                const float y = !masked || (col >= clo && col < chi) ? v[h * 16 + i] : -INFINITY;
+                x = fmaxf(x, y);
+              }
+              mx = fmaxf(mx, x == -INFINITY ? x : fmaf(x, sc.x, sc.y));
+            }
+          }
+          const bool move = mx > m + kA5Slack;
+          if (__any_sync(0xffffffffu, move)) {
+            const float nm = move ? mx : m;
+            const float al = move ? attn_ex2(m - nm) : 1.f;      // 0 where there was nothing
+            m = nm;
+            l *= al;
+            if (q > 0) {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                float v[32];
+                a5_ld32(to + c, v);
+                uint32_t r0[16], r1[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  r0[i] = __float_as_uint(v[i] * al);
+                  r1[i] = __float_as_uint(v[16 + i] * al);
+                }
+                a5_st16(to + c, r0);
+                a5_st16(to + c + 16, r1);
+              }
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            a5_ld32(ts + c * 32, v);
+            uint32_t pk[16];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float4 sc = a5_lds_f4(ssc + (c * 2 + h) * 16);
+              const float bb = sc.y - base;
+              float sum = 0.f;
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                const int col = c * 32 + h * 16 + i;
+                float w0 = attn_ex2(fmaf(v[h * 16 + i], sc.x, bb)), w1 = attn_ex2(fmaf(v[h * 16 + i + 1], sc.x, bb));
+                if (masked) {
+                  w0 = col >= clo && col < chi ? w0 : 0.f;
+                  w1 = col + 1 >= clo && col + 1 < chi ? w1 : 0.f;
+                }
+                sum += w0 + w1;
+                pk[h * 8 + i / 2] = a5_pack(w0, w1);
+              }
+              l = fmaf(sum, sc.z, l);
+            }
+            a5_st16(ts + c * 16, pk);                            // over columns of S that have been read
+          }
+          a5_wait_st();
+          t5_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pfull[s]);
+        }
+        jt += n;
+        if (ok) ok = mbar_wait(&ofull[s], items & 1, 0x52b);
+        ok = __all_sync(0xffffffffu, ok);
+        t5_fence_after();
+        ++items;
+        // ---------------------------------------------------------------- the item's result
+        const bool whole = w.u0 == 0 && w.u1 == it.units;
+        const int c0 = sp.owner(w.at), c1 = sp.owner(w.at + it.units - 1);
+        float* slots = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.workspace) + kAttnMaxCtas * 4);
+        constexpr size_t SLOT = attn_slot_floats(kA5R, D);
+        float* part = slots + SLOT * (2 * cta + (w.u0 == 0 ? 1 : 0));
+        // an item of one row tile: stream 1's sums come over through the (now idle) places of Q
+        float* xo = reinterpret_cast<float*>(smem + S::oQ);
+        float2* xml = reinterpret_cast<float2*>(smem + S::oMl);
+        float f0 = 1.f, f1 = 0.f;
+        if (!two) {
+          a5_sync_softmax();                                     // both streams' products are complete
+          if (s == 1) {
+            xml[tr] = make_float2(m, l);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float v[32];
+              if (nj > 0) {
+                a5_ld32(to + c, v);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0.f;
+              }
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4*>(xo + ((size_t)((c + i) / 4) * 128 + tr) * 4) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
+          }
+          a5_sync_softmax();
+          if (s == 0) {
+            const float2 y = xml[tr];
+            const float mm = fmaxf(m, y.x);
+            f0 = mm == -INFINITY ? 1.f : attn_ex2(m - mm);
+            f1 = mm == -INFINITY ? 1.f : attn_ex2(y.x - mm);
+            l = l * f0 + y.y * f1;
+            m = mm;
+          }
+        }
+        const bool mine = two || s == 0;                         // this stream writes rows
+        const bool some = l > 0.f || l != l;
+        const float inv = some ? __fdiv_rn(1.f, l) : 0.f;
+        auto put = [&](int c, const float (&v)[32], float scale) {
+          __half* dst = a.out + (long long)(it.start + gr / p.group) * a.out_stride + (long long)(it.h * p.group + gr % p.group) * D + c;
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(dst + i) =
+                make_uint4(a5_pack(v[i] * scale, v[i + 1] * scale), a5_pack(v[i + 2] * scale, v[i + 3] * scale),
+                           a5_pack(v[i + 4] * scale, v[i + 5] * scale), a5_pack(v[i + 6] * scale, v[i + 7] * scale));
+        };
+        auto put_lse = [&](float mm, float ll) {
+          if (a.lse)
+            a.lse[(long long)(it.start + gr / p.group) * a.q_heads + it.h * p.group + gr % p.group] =
+                ll > 0.f || ll != ll ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+        };
+        if (mine) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float v[32];
+            a5_ld32(to + c, v);
+            if (!two) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float4 y = *reinterpret_cast<const float4*>(xo + ((size_t)((c + i) / 4) * 128 + tr) * 4);
+                v[i] = fmaf(y.x, f1, v[i] * f0);
+                v[i + 1] = fmaf(y.y, f1, v[i + 1] * f0);
+                v[i + 2] = fmaf(y.z, f1, v[i + 2] * f0);
+                v[i + 3] = fmaf(y.w, f1, v[i + 3] * f0);
+              }
+            }
+            if (whole) {
+              if (valid) put(c, v, inv);
+            } else {
+              // [channel / 4][row]: a warp's stores are contiguous
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4*>(part + ((size_t)((c + i) / 4) * kA5R + off + tr) * 4) =
+                    make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
+          }
+          if (whole) {
+            if (valid) put_lse(m, l);
+          } else {
+            part[(size_t)kA5R * D + off + tr] = m;
+            part[(size_t)kA5R * D + kA5R + off + tr] = l;
+          }
+        }
+        if (!whole) {
+          // -------------------------------------------------------------- the last piece joins all of them
+          unsigned int* ticket = reinterpret_cast<unsigned int*>(a.workspace) + c0;
+          __threadfence();
+          a5_sync_softmax();
+          if (tid == 0) *flag = atomicAdd(ticket, 1u) == (unsigned)(c1 - c0);
+          a5_sync_softmax();
+          if (*flag && mine && valid) {
+            __threadfence();
+            float mm = -INFINITY, ll = 0.f;
+            for (int c = c0; c <= c1; ++c)
+              mm = fmaxf(mm, __ldcg(slots + SLOT * (2 * c + (c == c0 ? 1 : 0)) + (size_t)kA5R * D + off + tr));
+            const float b = mm == -INFINITY ? 0.f : mm;
+            for (int c = c0; c <= c1; ++c) {
+              const float* x = slots + SLOT * (2 * c + (c == c0 ? 1 : 0)) + (size_t)kA5R * D + off + tr;
+              ll = fmaf(__ldcg(x + kA5R), attn_ex2(__ldcg(x) - b), ll);
+            }
+            const float iv = ll > 0.f || ll != ll ? __fdiv_rn(1.f, ll) : 0.f;
+#pragma unroll 1
+            for (int ch = 0; ch < D; ch += 32) {
+              float v[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0.f;
+              for (int c = c0; c <= c1; ++c) {
+                const float* x = slots + SLOT * (2 * c + (c == c0 ? 1 : 0));
+                const float f = attn_ex2(__ldcg(x + (size_t)kA5R * D + off + tr) - b);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                  const float4 y = __ldcg(reinterpret_cast<const float4*>(x + ((size_t)((ch + i) / 4) * kA5R + off + tr) * 4));
+                  v[i] = fmaf(y.x, f, v[i]);
+                  v[i + 1] = fmaf(y.y, f, v[i + 1]);
+                  v[i + 2] = fmaf(y.z, f, v[i + 2]);
+                  v[i + 3] = fmaf(y.w, f, v[i + 3]);
+                }
+              }
+              put(ch, v, iv);
+            }
+            put_lse(mm, ll);
+          }
+          if (*flag && tid == 0) *ticket = 0;
+        }
+        if (!ok && lane == 0) *reinterpret_cast<volatile int*>(bad) = 1;
+        a5_sync_softmax();                                       // Q's places and the flag are free again
+        if (*reinterpret_cast<volatile int*>(bad)) break;
+        more = w.next(a, p.group);
+      }
+    }
+  }
+  t5_fence_before();
+  __syncthreads();
+  if (warp == 16) {
+    t5_fence_after();
+    t5_free512(tmem);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+template <int D>
+static cudaError_t launch_attn5_d(A5Params& p, cudaStream_t stream) {
+  auto kern = w4_attn5_kernel<D>;
+  static_assert(A5Smem<D>::kTotal <= 227 * 1024, "shared memory of one CTA");
+  static FuncAttrCache attrs;
+  cudaError_t ea = attrs.ensure(
+      [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, A5Smem<D>::kTotal); });
+  if (ea != cudaSuccess) return ea;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)device_sm_count());
+  cfg.blockDim = dim3(kA5Threads);
+  cfg.dynamicSmemBytes = A5Smem<D>::kTotal;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+  note_launch();
+  return e;
+}
+
+cudaError_t launch_attn5(const AttnArgs& a, cudaStream_t stream) {
+  A5Params p;
+  p.a = a;
+  p.group = a.q_heads / a.c.kv_heads;
+  p.max_blocks = (a.max_q * p.group + kA5R - 1) / kA5R;
+  p.min_units = 4;
+  return a.c.dim == 128 ? launch_attn5_d<128>(p, stream) : launch_attn5_d<64>(p, stream);
+}
+
+unsigned int read_clear_error_attn5() { return read_clear_error_word_here(); }
+
+}  // namespace w4

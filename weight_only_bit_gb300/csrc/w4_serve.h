@@ -48,7 +48,9 @@ struct AttnArgs {
   void* workspace;
 };
 int64_t attn_workspace_bytes(int tokens, int batch, int q_heads, int kv_heads, int head_dim);
+// Up to 32 rows (new tokens x query heads per kv head) of a sequence and kv head, and any number.
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_attn5(const AttnArgs& a, cudaStream_t stream);
 
 struct VerifyArgs {
   const __half *target, *draft;
@@ -68,5 +70,6 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream);
 // Each translation unit's device error word, read and cleared on the current device.
 unsigned int read_clear_error_kv();
 unsigned int read_clear_error_attn();
+unsigned int read_clear_error_attn5();
 
 }  // namespace w4

@@ -113,7 +113,7 @@ int w4_attn_kv8(const w4_kv_cache* cache, const uint16_t* q, uint16_t* out, floa
   if (s != W4_OK) return s;
   if (!q || !out || !workspace) return W4_ERR_NULL;
   if ((s = check_batch(a.c, q_start, kv_len, tokens, batch, q_heads, max_q)) != W4_OK) return s;
-  if (window < 0 || !std::isfinite(softmax_scale)) return W4_ERR_SHAPE;
+  if (window < 0 || !std::isfinite(softmax_scale) || softmax_scale <= 0.f) return W4_ERR_SHAPE;
   const int64_t dq = (int64_t)q_heads * a.c.dim;
   if ((s = check_stride(q_stride, dq, &a.q_stride)) != W4_OK || (s = check_stride(out_stride, dq, &a.out_stride)) != W4_OK)
     return s;

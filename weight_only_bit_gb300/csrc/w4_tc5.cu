@@ -45,6 +45,7 @@
 #include "w4_common.cuh"
 #include "w4_decode.cuh"
 #include "w4_internal.h"
+#include "w4_t5.cuh"
 
 namespace w4 {
 
@@ -90,28 +91,12 @@ __host__ __device__ constexpr uint32_t t5_idesc() {
   return (1u << 4) | ((uint32_t)(NB >> 3) << 17) | ((uint32_t)(kT5Rows >> 4) << 24);
 }
 
-// D[tmem] (+)= A[tmem] . B[smem]^T, M = 128, K = 16.
-__device__ __forceinline__ void t5_mma_ts(uint32_t dtmem, uint32_t atmem, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-      ::"r"(dtmem), "r"(atmem), "l"(bdesc), "r"(idesc), "r"(acc) : "memory");
-}
-
 // This warp's 32 lanes x 8 consecutive columns of tensor memory <- 8 registers per thread.
 __device__ __forceinline__ void t5_st8(uint32_t taddr, const uint32_t (&v)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
                ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
-
-__device__ __forceinline__ void t5_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-               ::"r"(smem_u32(bar)) : "memory");
-}
-
-__device__ __forceinline__ void t5_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void t5_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
 // 16 consecutive FP32 columns of this thread's tensor-memory lane.
 __device__ __forceinline__ void t5_ld16(uint32_t taddr, float (&v)[16]) {
@@ -285,9 +270,7 @@ __global__ void __launch_bounds__(kT5Threads, 1) w4_tc5_kernel(const __grid_cons
     fence_mbar_init();
   }
   if (warp == kT5Mw) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                 ::"r"(smem_u32(tmem_slot)), "r"(512) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    t5_alloc512(tmem_slot);
   }
   t5_fence_before();
   __syncthreads();
@@ -564,7 +547,7 @@ __global__ void __launch_bounds__(kT5Threads, 1) w4_tc5_kernel(const __grid_cons
   }
   if (warp == kT5Mw) {
     t5_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    t5_free512(tmem);
   }
 }
 
