@@ -39,6 +39,7 @@ namespace w4 {
 constexpr int kAtT = 32;                     // keys per unit
 constexpr int kAtWarps = 8;
 constexpr int kAtThreads = kAtWarps * 32;
+constexpr int kAtOv = 4;                     // what an item costs beside its units
 constexpr float kAtSlack = 6.f;
 
 template <int D, int NT>
@@ -61,7 +62,7 @@ struct AtSmem {
 struct AtParams {
   AttnArgs a;
   CUtensorMap tk, tv;      // [pages][heads * page][D], box D x min(page, 32) x 1
-  int group, max_blocks, min_units;
+  int group;
 };
 
 __device__ __forceinline__ void at_tma3(uint32_t dst, const CUtensorMap* map, int c1, int c2, uint64_t* bar, uint64_t pol) {
@@ -142,30 +143,30 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
   }
   pdl_launch_dependents();
   pdl_wait();
-  const Split sp = attn_split<R, kAtT>(a, p.group, p.max_blocks, p.min_units, (int)gridDim.x, prefix);
+  const Split sp = attn_split<kAtT, kAtOv>(a, a.max_q, 2 * kAtWarps, (int)gridDim.x, prefix);
   const int cta = (int)blockIdx.x;
   if (cta >= sp.ctas || sp.U == 0) return;
   const int begin = sp.first(cta), end = sp.first(cta + 1);
   if (begin >= end) return;
-  Walk<R, kAtT> w;
-  w.start(a, p.group, prefix, begin, end);
+  Walk<kAtT, kAtOv> w;
+  if (!w.start(a, a.max_q, prefix, begin, end)) return;
   __syncthreads();                           // the prefix sums' place becomes the merge buffer
   const float c2 = a.scale * 1.4426950408889634f;
   const uint64_t pol = policy_evict_first();
-  const int mine = (end - begin - warp + kAtWarps - 1) / kAtWarps;    // this warp's units: begin + warp + 8 i
+  // this warp's units: warp + 8 i of the CTA's tiles
 
   // ---- loading: lane (i, s) = (lane / 2, lane % 2) knows 16-key group s of unit 16 * batch + i
   const int P = a.c.page;
   const int sub = lane & 1;
   const int per = P >= kAtT ? 2 : 1;         // 16-key groups per box
-  Walk<R, kAtT> ahead = w;                   // walks with the batches: each lane to its own unit
+  Walk<kAtT, kAtOv> ahead = w;               // walks with the batches: each lane to its own unit
+  bool left = true;                          // the lane's walk has not ended
   auto look = [&](int batch) {
     AtGroup g{-1, 0, 0.f, 0.f, 1.f};
-    const int i = batch * 16 + (lane >> 1);
-    if (i < mine) {
-      const int target = begin + warp + kAtWarps * i;
-      while (target >= ahead.at + ahead.it.units && ahead.next(a, p.group)) {}
-      const int key = (ahead.it.t0 + target - ahead.at) * kAtT + 16 * sub;
+    const int unit = warp + kAtWarps * (batch * 16 + (lane >> 1));
+    while (left && unit >= ahead.base + ahead.u1 - ahead.u0) left = ahead.next(a, a.max_q);
+    if (left) {
+      const int key = (ahead.it.t0 + ahead.u0 + unit - ahead.base) * kAtT + 16 * sub;
       if (key < ahead.it.hi && key + 16 > ahead.it.lo) {
         const int page = __ldg(a.c.table + (long long)ahead.it.b * a.c.table_stride + key / P);
         if (page < 0 || page >= a.c.num_pages) {
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
       }
     }
   };
-  for (int i = 0; i < min(NST, mine); ++i) issue(i, cur);
+  for (int i = 0; i < NST; ++i) issue(i, cur);       // units past the end: nothing to load, nobody waits
 
   // ---- computing
   const int g = lane >> 2, t = lane & 3;
@@ -217,12 +218,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int row = it.rb * R + n * 8 + 2 * t + e;
+        const int row = n * 8 + 2 * t + e;
         const int pos = row < it.n * p.group ? shift + row / p.group : -1;
         rhi[n][e] = pos < 0 ? 0 : a.causal ? min(it.total, pos + 1) : it.total;
         rlo[n][e] = a.window > 0 ? pos - a.window + 1 : 0;
       }
-      const int row = it.rb * R + n * 8 + g;         // B column g
+      const int row = n * 8 + g;                     // B column g
       const bool valid = row < it.n * p.group;
       const __half* q = a.q + (long long)(it.start + row / p.group) * a.q_stride + (long long)(it.h * p.group + row % p.group) * D;
 #pragma unroll
@@ -244,18 +245,17 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
         for (int e = 0; e < 4; ++e) o[n][x][e] = 0.f;
     }
     // keys that every row of the item sees need no mask
-    const int pfirst = shift + it.rb * R / p.group;
-    const int plast = shift + min((it.rb * R + R - 1) / p.group, it.n - 1);
+    const int pfirst = shift, plast = it.total - 1;
     const int full_lo = a.window > 0 ? max(it.lo, plast - a.window + 1) : it.lo;
     const int full_hi = pfirst < 0 ? 0 : (a.causal ? min(it.hi, pfirst + 1) : it.hi);
 
-    const int stop = w.at + w.u1 - begin;            // of this item, counted in the CTA's units
+    const int stop = w.base + w.u1 - w.u0;           // of this item, counted in the CTA's units
     for (; warp + kAtWarps * i < stop; ++i) {
       const int st = i % NST;
       if ((i & 15) == 0) nxt = look(i / 16 + 1);      // in flight while these 16 are computed
       if (ok) ok = mbar_wait(&full[st], (i / NST) & 1, 0x512);
       ok = __all_sync(0xffffffffu, ok);
-      const int k0 = (it.t0 + begin + warp + kAtWarps * i - w.at) * kAtT;
+      const int k0 = (it.t0 + w.u0 + warp + kAtWarps * i - w.base) * kAtT;
       const uint32_t sk = ring + st * S::kStage, sv = sk + kAtT * D;
       const bool masked = k0 < full_lo || k0 + kAtT > full_hi;
       float s[NT][2][4];                             // [tile][16 keys][A rows g, g + 8 x B columns 2t, 2t + 1]
@@ -376,10 +376,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
         }
       }
       __syncwarp();                                  // every lane has read the stage
-      if (i + NST < mine) {
-        if (((i + NST) & 15) < NST && (i + NST) / 16 != i / 16) issue(i + NST, nxt);
-        else issue(i + NST, cur);
-      }
+      if ((i + NST) / 16 != i / 16) issue(i + NST, nxt);
+      else issue(i + NST, cur);
       if ((i & 15) == 15) cur = nxt;
     }
 
@@ -440,16 +438,15 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
           }
     }
     __syncthreads();
-    const bool whole = w.u0 == 0 && w.u1 == it.units;
-    const int c0 = sp.owner(w.at), c1 = sp.owner(w.at + it.units - 1);
+    const bool whole = w.whole();
+    const int c0 = w.first_cta(sp), c1 = w.last_cta(sp);
     float* slots = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.workspace) + kAttnMaxCtas * 4);
     constexpr size_t SLOT = attn_slot_floats(R, D);
     float* part = slots + SLOT * (2 * cta + (w.u0 == 0 ? 1 : 0));
     auto store = [&](int row, int ch, float4 v, float mm, float ll) {
       // one row's four channels of the finished item
-      const int gr = it.rb * R + row;
-      if (gr >= it.n * p.group) return;
-      const int r = gr / p.group, head = it.h * p.group + gr % p.group;
+      if (row >= it.n * p.group) return;
+      const int r = row / p.group, head = it.h * p.group + row % p.group;
       const bool some = ll > 0.f || ll != ll;
       const float inv = some ? __fdiv_rn(1.f, ll) : 0.f;
       const uint2 u = make_uint2(at_pack(v.x * inv, v.y * inv), at_pack(v.z * inv, v.w * inv));
@@ -495,7 +492,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
         __threadfence();
         for (int e = tid; e < R * (D / 4); e += kAtThreads) {
           const int row = e / (D / 4), ch = e % (D / 4);
-          if (it.rb * R + row >= it.n * p.group) continue;
+          if (row >= it.n * p.group) continue;
           float mm = -INFINITY;
           for (int c = c0; c <= c1; ++c)
             mm = fmaxf(mm, __ldcg(slots + SLOT * (2 * c + (c == c0 ? 1 : 0)) + (size_t)R * D + row));
@@ -518,7 +515,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
         if (tid == 0) *ticket = 0;
       }
     }
-    more = w.next(a, p.group);
+    more = w.next(a, a.max_q);
+  }
+  if (!ok) {                                         // a lost wait: the copies in flight must land all the same
+    for (int k = i; k < i + NST; ++k) mbar_wait(&full[k % NST], (k / NST) & 1, 0x519);
   }
 }
 
@@ -537,9 +537,6 @@ static cudaError_t launch_attn_nt(AtParams& p, cudaStream_t stream) {
       [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, AtSmem<D, NT>::kTotal); });
   if (ea != cudaSuccess) return ea;
   static_assert(AtSmem<D, NT>::kTotal <= 227 * 1024, "shared memory of one CTA");
-  const int rows = p.a.max_q * p.group;
-  p.max_blocks = (rows + 8 * NT - 1) / (8 * NT);
-  p.min_units = 2 * kAtWarps;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)device_sm_count());
   cfg.blockDim = dim3(kAtThreads);

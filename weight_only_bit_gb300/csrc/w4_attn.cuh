@@ -1,14 +1,14 @@
 // w4_attn.cuh -- what the attention kernels share: the device-side split of ragged work over the CTAs,
 // and the join of the pieces.
 //
-// Work.  An item is (sequence, kv head, block of R rows); its rows are the (new token, query head of
-// the group) pairs in that order.  Its keys are the unit-aligned range [lo, hi) that any of its rows
-// sees, counted in units of T tokens, at least one unit (an item without keys still writes its rows).
-// All units of all items, in the order (sequence, head, block, key), are cut into equal consecutive
-// ranges, one per CTA: a long cache is split over many CTAs, many short ones share one, and no CTA
-// has more than one unit above another, whatever the mix of lengths.  The lengths are on the device,
-// so each CTA computes the split itself (prefix sums over the sequences in shared memory).
-// An item whose units lie in several CTAs is joined by the last of them to finish (a ticket in the
+// Work.  An item is (sequence, kv head, block of `tpb` new tokens with all query heads of the group).
+// Its keys are the tile-aligned range [lo, hi) that any of its rows sees, counted in tiles of T keys, at
+// least one (an item without keys still writes its rows).  An item costs its tiles and OV more, what
+// beginning and ending one costs in tiles.  The cost of all items, in the order (sequence, head,
+// block, key), is cut into equal consecutive ranges, one per CTA: a long cache is split over many
+// CTAs, many short ones share one, whatever the mix of lengths.  The lengths are on the device, so each
+// CTA computes the split itself (prefix sums over the sequences in shared memory).
+// An item whose tiles lie in several CTAs is joined by the last of them to finish (a ticket in the
 // workspace), over the pieces in key order: the result does not depend on which one is last.
 #pragma once
 #include <cstdint>
@@ -29,10 +29,10 @@ __device__ __forceinline__ float attn_ex2(float x) {
 }
 
 struct Item {
-  int b, h, rb;        // sequence, kv head, row block
+  int b, h, rb;        // sequence, kv head, token block
   int start, n, total; // first row of the sequence, its rows, its tokens in the cache
   int lo, hi;          // keys [lo, hi) that any row of the block sees (lo == hi: none)
-  int t0, units;       // first unit of the range, units (at least 1)
+  int t0, tiles;       // first tile of the range, tiles (at least 1)
 };
 
 // One sequence's numbers; what does not fit the caller's promise counts as no rows.
@@ -49,11 +49,11 @@ __device__ __forceinline__ void item_seq(const AttnArgs& a, Item& it, int b, boo
   }
 }
 
-template <int R, int T>
-__device__ __forceinline__ void item_block(const AttnArgs& a, Item& it, int group, int rb) {
+template <int T>
+__device__ __forceinline__ void item_block(const AttnArgs& a, Item& it, int tpb, int rb) {
   it.rb = rb;
-  const int i0 = rb * R / group;
-  const int i1 = min((rb * R + R - 1) / group, it.n - 1);
+  const int i0 = rb * tpb;
+  const int i1 = min(i0 + tpb, it.n) - 1;
   const int shift = it.total - it.n;
   int hi = a.causal ? min(it.total, shift + i1 + 1) : (shift + i1 >= 0 ? it.total : 0);
   int lo = a.window > 0 ? max(0, shift + i0 - a.window + 1) : 0;
@@ -61,34 +61,33 @@ __device__ __forceinline__ void item_block(const AttnArgs& a, Item& it, int grou
   it.lo = lo;
   it.hi = hi;
   it.t0 = lo / T;
-  it.units = hi > lo ? (hi + T - 1) / T - it.t0 : 1;
+  it.tiles = hi > lo ? (hi + T - 1) / T - it.t0 : 1;
 }
 
-template <int R>
-__device__ __forceinline__ int item_blocks(const Item& it, int group) { return (it.n * group + R - 1) / R; }
+__device__ __forceinline__ int item_blocks(const Item& it, int tpb) { return (it.n + tpb - 1) / tpb; }
 
-// The split: prefix[b] = units of the sequences before b; U = all units; ctas = CTAs that get work.
+// The split of the whole cost U over the CTAs that get work.
 struct Split {
   int U, ctas;
   __device__ __forceinline__ int first(int c) const { return (int)((long long)c * U / ctas); }
-  // The CTA that unit u belongs to: the smallest c with first(c + 1) > u.
+  // The CTA that cost position u belongs to: the smallest c with first(c + 1) > u.
   __device__ __forceinline__ int owner(int u) const { return (int)((((long long)u + 1) * ctas - 1) / U); }
 };
 
-// By all threads of the CTA: fills prefix[0 ... batch] (shared) and returns the split.  min_units: a CTA
-// gets at least about that many (fewer CTAs share little work, so that less is joined).
-template <int R, int T>
-__device__ __forceinline__ Split attn_split(const AttnArgs& a, int group, int max_blocks, int min_units, int ctas,
-                                            int* prefix) {
+// By all threads of the CTA: fills prefix[0 ... batch] (shared; the cost of the sequences before each) and
+// returns the split.  least: a CTA gets at least about that much (fewer CTAs share little work, so
+// that less is joined).
+template <int T, int OV>
+__device__ __forceinline__ Split attn_split(const AttnArgs& a, int tpb, int least, int ctas, int* prefix) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
-  if (max_blocks == 1) {
+  if (a.max_q <= tpb) {                      // one block per sequence: a thread each
     for (int b = tid; b < a.batch; b += nt) {
       Item it;
       item_seq(a, it, b, blockIdx.x == 0);
       int s = 0;
       if (it.n > 0) {
-        item_block<R, T>(a, it, group, 0);
-        s = it.units * a.c.kv_heads;
+        item_block<T>(a, it, tpb, 0);
+        s = (it.tiles + OV) * a.c.kv_heads;
       }
       prefix[b + 1] = s;
     }
@@ -96,11 +95,11 @@ __device__ __forceinline__ Split attn_split(const AttnArgs& a, int group, int ma
     for (int b = tid >> 5; b < a.batch; b += nt >> 5) {
       Item it;
       item_seq(a, it, b, blockIdx.x == 0 && lane == 0);
-      const int nb = item_blocks<R>(it, group);
+      const int nb = item_blocks(it, tpb);
       int s = 0;
       for (int rb = lane; rb < nb; rb += 32) {
-        item_block<R, T>(a, it, group, rb);
-        s += it.units;
+        item_block<T>(a, it, tpb, rb);
+        s += it.tiles + OV;
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -126,45 +125,41 @@ __device__ __forceinline__ Split attn_split(const AttnArgs& a, int group, int ma
   __syncthreads();
   Split s;
   s.U = prefix[a.batch];
-  s.ctas = max(1, min(ctas, (s.U + min_units - 1) / min_units));
+  s.ctas = max(1, min(ctas, (s.U + least - 1) / least));
   return s;
 }
 
-// A CTA's walk over its units: the current item, its place in the whole order, and this CTA's part
-// [u0, u1) of the item's units.  Every warp walks for itself (all lanes together).
-template <int R, int T>
+// A CTA's walk over its items: the current one, where it lies in the whole cost, and this CTA's tiles
+// [u0, u1) of it.  Every warp walks for itself; start() needs all its lanes, next() does not.
+template <int T, int OV>
 struct Walk {
   Item it;
-  int at;              // global index of the item's unit 0
-  int u0, u1;          // this CTA's units of the item, counted in the item
-  int end;             // global end of this CTA's range
-  int blocks;
+  int at;              // cost position of the item
+  int u0, u1;          // this CTA's tiles of the item, counted in the item
+  int base;            // tiles of this CTA before them
+  int end;             // end of this CTA's range
 
-  __device__ __forceinline__ void clip(int begin) {
-    u0 = max(begin - at, 0);
-    u1 = min(end - at, it.units);
-  }
-  // Starts at global unit `begin` (< end).
-  __device__ __forceinline__ void start(const AttnArgs& a, int group, const int* prefix, int begin, int end_) {
+  // Starts at cost position `begin` (< end_); false if the range holds no tile.
+  __device__ __forceinline__ bool start(const AttnArgs& a, int tpb, const int* prefix, int begin, int end_) {
     const int lane = threadIdx.x & 31;
     end = end_;
-    int lo = 0, hi = a.batch - 1;            // the last b with prefix[b] <= begin (and units after it)
+    base = 0;
+    int lo = 0, hi = a.batch - 1;            // the last b with prefix[b] <= begin (and a cost of its own)
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (prefix[mid] <= begin) lo = mid; else hi = mid - 1;
     }
     item_seq(a, it, lo, false);
-    blocks = item_blocks<R>(it, group);
+    const int blocks = item_blocks(it, tpb);
     const int per = (prefix[lo + 1] - prefix[lo]) / a.c.kv_heads;
-    const int rem = begin - prefix[lo];
-    it.h = rem / per;
+    it.h = (begin - prefix[lo]) / per;
     at = prefix[lo] + it.h * per;
-    // the row block: scan of the blocks' units, 32 at a time
+    // the token block: scan of the blocks' costs, 32 at a time
     for (int r0 = 0;; r0 += 32) {
       int u = 0;
       if (r0 + lane < blocks) {
-        item_block<R, T>(a, it, group, r0 + lane);
-        u = it.units;
+        item_block<T>(a, it, tpb, r0 + lane);
+        u = it.tiles + OV;
       }
       int v = u;
 #pragma unroll
@@ -176,36 +171,43 @@ struct Walk {
       if (past != 0 || r0 + 32 >= blocks) {
         const int k = past ? __ffs(past) - 1 : 31;
         at += __shfl_sync(0xffffffffu, v - u, k);
-        item_block<R, T>(a, it, group, r0 + k);
+        item_block<T>(a, it, tpb, r0 + k);
         break;
       }
       at += __shfl_sync(0xffffffffu, v, 31);
     }
-    clip(begin);
+    u0 = max(begin - at - OV, 0);
+    u1 = min(end - at - OV, it.tiles);
+    return u1 > u0;
   }
   // The next item; false when the range is done.
-  __device__ __forceinline__ bool next(const AttnArgs& a, int group) {
-    at += it.units;
-    if (at >= end) return false;
+  __device__ __forceinline__ bool next(const AttnArgs& a, int tpb) {
+    const int past = at + OV + it.tiles;
+    if (past + OV >= end) return false;
+    base += u1 - u0;
+    at = past;
     int rb = it.rb + 1;
-    if (rb >= blocks) {
+    if (rb * tpb >= it.n) {
       rb = 0;
       if (++it.h >= a.c.kv_heads) {
         it.h = 0;
         do item_seq(a, it, it.b + 1, false); while (it.n <= 0);
-        blocks = item_blocks<R>(it, group);
       }
     }
-    item_block<R, T>(a, it, group, rb);
-    clip(0);
+    item_block<T>(a, it, tpb, rb);
     u0 = 0;
+    u1 = min(end - at - OV, it.tiles);
     return true;
   }
+  __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == it.tiles; }
+  // The CTAs that hold the item's first and last tile.
+  __device__ __forceinline__ int first_cta(const Split& s) const { return s.owner(at + OV); }
+  __device__ __forceinline__ int last_cta(const Split& s) const { return s.owner(at + OV + it.tiles - 1); }
 };
 
-// Workspace: one ticket per CTA (of the item that starts in the CTA and goes on after it), then two
-// partial results per CTA: slot 2c of an item that began before CTA c, 2c + 1 of one that begins in it
-// and goes on.  A partial result: R rows of D sums, R maxima, R sums of weights.
+// Workspace: one ticket per CTA (of the item whose first tile lies in the CTA and that goes on after it),
+// then two partial results per CTA: slot 2c of an item that began before CTA c, 2c + 1 of one that
+// begins in it and goes on.  A partial result: R rows of D sums, R maxima, R sums of weights.
 constexpr int kAttnMaxCtas = 1024;
 __host__ __device__ constexpr size_t attn_slot_floats(int R, int D) { return (size_t)R * (D + 2); }
 

@@ -7,20 +7,24 @@
 // products that the work is a dense contraction: S = Q K^T and O += P V, both M = 128, FP16 x FP16 ->
 // FP32 with the accumulators in tensor memory.
 //
-// An item has up to 256 rows: two row tiles of 128, each with its own S, O and softmax warpgroup
-// ("streams").  An item of at most 128 rows gives both streams the same rows and every second key
-// tile each, joined at the end; so the two softmax warpgroups always overlap the other's products.
+// A row tile is as many whole tokens (all query heads of the group) as fit 128 rows, one TMA box of q.
+// An item has up to two row tiles, each with its own S, O and softmax warpgroup ("streams").  An item
+// of one row tile gives both streams the same rows and every second key tile each, joined at the
+// end; so the two softmax warpgroups always overlap the other's products.
 // Tensor memory is full: S 2 x 128 columns, O 2 x D columns (256 at D = 128); the weights P go back
 // over the first half of their S as FP16, the A operand of the second product.
-// Roles (17 warps), connected by mbarriers:
-//   warps 0-3, 4-7   softmax of stream 0 and 1: a thread per row.  Load Q, then per key tile: maximum,
-//                    weights, sums, P; O is rescaled in place when the bound moved; at the end out.
-//   warps 8-11       keys: codes from global memory, FP16 into the canonical K-major layout
-//   warps 12-15      values: the same into the MN-major layout (channels contiguous, as they lie in
-//                    memory: nothing is transposed)
-//   warp 16          issues the MMAs: PV of a stream, then its next S, alternating between streams
+// Roles (13 warps, so that a thread may hold 128 registers), connected by mbarriers:
+//   warps 0-3, 4-7   softmax of stream 0 and 1: a thread per row, one pass over its S: 32 keys at a time,
+//                    their maximum, then weights, sums, P.  Where a maximum passes the bound (the
+//                    first keys of an item, rarely later), O and the P written so far are rescaled in
+//                    place.  At the end out.
+//   warps 8-11       codes from global memory, FP16 into shared memory: keys in the canonical K-major
+//                    layout, values in the MN-major one (channels contiguous, as they lie in
+//                    memory: nothing is transposed).  A tile's loads are issued a tile ahead.
+//   warp 12          issues the MMAs: PV of a stream, then its next S, alternating between streams
 // What bounds it: figures beside the launch below.
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -33,10 +37,17 @@
 namespace w4 {
 
 constexpr int kA5T = 128;                    // keys per tile
-constexpr int kA5R = 256;                    // rows per item
-constexpr int kA5Threads = 17 * 32;
+constexpr int kA5R = 256;                    // rows per item, at most
+constexpr int kA5Ov = 2;                     // what an item costs beside its tiles
+constexpr int kA5Mma = 12;                   // the issuing warp
+constexpr int kA5Threads = (kA5Mma + 1) * 32;
 constexpr float kA5Slack = 6.f;
 constexpr int kA5ScaleSlots = 4;
+
+template <bool B>
+struct A5Flag {
+  static constexpr bool value = B;
+};
 
 template <int D>
 struct A5Smem {
@@ -55,7 +66,8 @@ struct A5Smem {
 
 struct A5Params {
   AttnArgs a;
-  int group, max_blocks, min_units;
+  CUtensorMap tq;          // [tokens][heads][D], box of tpt x group rows of 64 channels
+  int group, tpt;          // query heads per kv head, tokens per row tile
 };
 
 // Shared-memory matrix descriptors (version 1, 128-byte swizzle).  K-major: rows of 128 bytes, 8-row
@@ -74,19 +86,20 @@ __host__ __device__ constexpr uint32_t a5_idesc(int N, bool mn) {
   return (1u << 4) | (mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
 }
 
+// 32 columns of this thread's lane: issued, and in the registers once a5_wait32 has passed.
 __device__ __forceinline__ void a5_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
       "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void a5_wait32(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]) :: "memory");
+}
+__device__ __forceinline__ void a5_get32(uint32_t taddr, float (&v)[32]) {
+  a5_ld32(taddr, v);
+  a5_wait32(v);
 }
 
 __device__ __forceinline__ void a5_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -126,7 +139,27 @@ __device__ __forceinline__ float4 a5_lds_f4(uint32_t a) {
 // Generic shared-memory writes before, tensor-core reads after.
 __device__ __forceinline__ void a5_fence_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void a5_sync_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ void a5_sync_stream(int s) { asm volatile("bar.sync %0, 128;" ::"r"(2 + s) : "memory"); }
+
+__device__ __forceinline__ void a5_tma3(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)) : "memory");
+}
+
+// Two FP32 operations in one instruction.
+__device__ __forceinline__ float2 a5_fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 a5_add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_constant__ A5Params p) {
@@ -134,14 +167,14 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
-  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + S::oBar);   // 4 key warps
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + S::oBar);   // 4 decoding warps
   uint64_t* kempty = kfull + 2;                                   // commit
   uint64_t* vfull = kempty + 2;
   uint64_t* vempty = vfull + 2;
-  uint64_t* scfull = vempty + 2;                                  // 4 key warps
+  uint64_t* scfull = vempty + 2;                                  // 4 decoding warps
   uint64_t* sfull = scfull + kA5ScaleSlots;                       // commit: S of the stream is there
   uint64_t* pfull = sfull + 2;                                    // 4 softmax warps: P of the stream is there
-  uint64_t* qfull = pfull + 2;                                    // 4 softmax warps: Q of the stream is there
+  uint64_t* qfull = pfull + 2;                                    // TMA: Q of the stream is there
   uint64_t* ofull = qfull + 2;                                    // commit: O of the stream is complete
   uint64_t* done = ofull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::oFlag);
@@ -158,7 +191,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
       mbar_init(&vempty[i], 1);
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], 4);
-      mbar_init(&qfull[i], 4);
+      mbar_init(&qfull[i], 1);
       mbar_init(&ofull[i], 1);
     }
     for (int i = 0; i < kA5ScaleSlots; ++i) mbar_init(&scfull[i], 4);
@@ -166,33 +199,28 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
     *bad = 0;
     fence_mbar_init();
   }
-  if (warp == 16) t5_alloc512(tmem_slot);
+  if (warp == kA5Mma) t5_alloc512(tmem_slot);
   t5_fence_before();
   __syncthreads();
   t5_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_launch_dependents();
   pdl_wait();
-  const Split sp = attn_split<kA5R, kA5T>(a, p.group, p.max_blocks, p.min_units, (int)gridDim.x, prefix);
+  const Split sp = attn_split<kA5T, kA5Ov>(a, 2 * p.tpt, 4 + kA5Ov, (int)gridDim.x, prefix);
   const int cta = (int)blockIdx.x;
   const int begin = cta < sp.ctas && sp.U > 0 ? sp.first(cta) : 0, end = cta < sp.ctas && sp.U > 0 ? sp.first(cta + 1) : 0;
   bool ok = true;
-  if (begin < end) {
-    Walk<kA5R, kA5T> w;
-    w.start(a, p.group, prefix, begin, end);
+  const int tpb = 2 * p.tpt;
+  Walk<kA5T, kA5Ov> w;
+  if (begin < end && w.start(a, tpb, prefix, begin, end)) {
     const float c2 = a.scale * 1.4426950408889634f;
-    if (warp >= 8 && warp < 16) {
-      // ================================================================ keys or values into shared memory
-      const bool is_v = warp >= 12;
+    if (warp >= 8 && warp < kA5Mma) {
+      // ================================================================ keys and values into shared memory
       const int wq = warp & 3;                       // rows 32 wq ... + 31 of the tile
       constexpr int LPR = D / 16;                    // lanes per row
       constexpr int RPI = 32 / LPR;                  // rows per pass of the warp
       constexpr int NP = 32 / RPI;                   // passes
       const int l = lane % LPR, rl = lane / LPR;
-      const uint8_t* pool = is_v ? a.c.v : a.c.k;
-      uint64_t* full = is_v ? vfull : kfull;
-      uint64_t* empty = is_v ? vempty : kempty;
-      const uint32_t base = sb + (is_v ? S::oV : S::oK);
       const int P = a.c.page;
       int u = w.u0, j = 0;
       bool more = true;
@@ -211,9 +239,9 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         }
         return page;
       };
-      uint4 data[NP];
-      float4 sc = make_float4(0.f, 0.f, 1.f, 0.f);
-      // issues the loads of the tile at (w, u); its scales too (key warps)
+      uint4 dk[NP], dv[NP];
+      float4 sc = make_float4(1.f, 0.f, 1.f, 0.f);
+      // issues the loads of the tile at (w, u), its scales too
       auto load = [&](int page) {
         const int k0 = (w.it.t0 + u) * kA5T + wq * 32;
         const int pg0 = __shfl_sync(0xffffffffu, page, 0), pg1 = __shfl_sync(0xffffffffu, page, 1);
@@ -223,58 +251,69 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
           const int key = k0 + r;
           const int pg = r < 16 ? pg0 : pg1;
           // rows that nobody sees are zero: their weights are 0, and 0 times a stale NaN would not be
-          data[i] = make_uint4(0, 0, 0, 0);
-          if (pg >= 0 && key >= w.it.lo && key < w.it.hi)
-            data[i] = ld_nc_v4(pool + (long long)pg * a.c.page_stride + (long long)(w.it.h * P + key % P) * D + 16 * l);
-        }
-        if (!is_v) {
-          sc = make_float4(0.f, 0.f, 1.f, 0.f);
-          if (lane < 2 && page >= 0) {
-            sc.x = __ldg(a.c.k_scale + (long long)page * a.c.scale_stride + w.it.h) * c2;
-            const float vs = __ldg(a.c.v_scale + (long long)page * a.c.scale_stride + w.it.h);
-            sc.y = log2f(vs);
-            sc.z = __fdiv_rn(1.f, vs);
+          dk[i] = dv[i] = make_uint4(0, 0, 0, 0);
+          if (pg >= 0 && key >= w.it.lo && key < w.it.hi) {
+            const long long at = (long long)pg * a.c.page_stride + (long long)(w.it.h * P + (key & (P - 1))) * D + 16 * l;
+            dk[i] = ld_nc_v4(a.c.k + at);
+            dv[i] = ld_nc_v4(a.c.v + at);
           }
+        }
+        sc = make_float4(1.f, 0.f, 1.f, 0.f);
+        if (lane < 2 && page >= 0) {
+          sc.x = __ldg(a.c.k_scale + (long long)page * a.c.scale_stride + w.it.h) * c2;
+          const float vs = __ldg(a.c.v_scale + (long long)page * a.c.scale_stride + w.it.h);
+          sc.y = log2f(vs);
+          sc.z = __fdiv_rn(1.f, vs);
+        }
+      };
+      // 16-byte chunks 2 (l % 4) and the next of the row's 128 bytes; half of the lanes begin with the
+      // second, so that a quarter-warp's stores meet all banks once
+      const bool second = (l >> 2) & 1;
+      const uint32_t ca = 2 * (l & 3) + (second ? 1 : 0), cb = ca ^ 1;
+      const uint32_t at = (uint32_t)(l >> 2) * 16384 + (uint32_t)(wq * 32 + rl) * 128;
+      auto decode = [&](uint32_t base, const uint4 (&d)[NP]) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const uint32_t r = (uint32_t)(i * RPI + rl) & 7u;
+          uint4 x0, x1;
+          a5_cvt16(d[i], x0, x1);
+          const uint32_t row = base + at + i * RPI * 128;
+          a5_sts128(row + ((ca ^ r) << 4), second ? x1 : x0);
+          a5_sts128(row + ((cb ^ r) << 4), second ? x0 : x1);
         }
       };
       load(pages_of(true));
       while (more && ok) {
         // the next tile's pages, while this one's data are on their way
         if (++u >= w.u1) {
-          more = w.next(a, p.group);
+          more = w.next(a, tpb);
           u = w.u0;
         }
         const int page = pages_of(more);
         const int st = j & 1;
-        if (j >= 2) ok = mbar_wait(&empty[st], ((j >> 1) - 1) & 1, is_v ? 0x521 : 0x522);
+        if (j >= 2) ok = mbar_wait(&kempty[st], ((j >> 1) - 1) & 1, 0x521);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t dst = base + st * S::kTile + ((16 * l) / 64) * 16384;
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const int r = wq * 32 + i * RPI + rl;
-          uint4 x[2];
-          a5_cvt16(data[i], x[0], x[1]);
-          // 16-byte chunks 2 (l % 4) and the next of the row's 128 bytes; half of the lanes begin with
-          // the second, so that a quarter-warp's stores meet all banks once
-          const int first = (l >> 2) & 1;
-          const uint32_t row = dst + r * 128;
-          const int c = 2 * (l & 3);
-          a5_sts128(row + (((c + first) ^ (r & 7)) << 4), x[first]);
-          a5_sts128(row + (((c + 1 - first) ^ (r & 7)) << 4), x[1 - first]);
-        }
-        if (!is_v && lane < 2)
+        decode(sb + S::oK + st * S::kTile, dk);
+        if (lane < 2)
           *reinterpret_cast<float4*>(smem + S::oScales + ((j & (kA5ScaleSlots - 1)) * 8 + wq * 2 + lane) * 16) = sc;
         a5_fence_proxy();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&full[st]);
-          if (!is_v) mbar_arrive(&scfull[j & (kA5ScaleSlots - 1)]);
+          mbar_arrive(&kfull[st]);
+          mbar_arrive(&scfull[j & (kA5ScaleSlots - 1)]);
         }
+        if (j >= 2) ok = mbar_wait(&vempty[st], ((j >> 1) - 1) & 1, 0x522);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        decode(sb + S::oV + st * S::kTile, dv);
+        a5_fence_proxy();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&vfull[st]);
         ++j;
         if (more) load(page);
       }
-    } else if (warp == 16) {
+    } else if (warp == kA5Mma) {
       // ================================================================ MMA issuer
       if (lane == 0) {
         constexpr uint32_t id_s = a5_idesc(128, false), id_o = a5_idesc(D, true);
@@ -283,7 +322,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         bool more = true;
         while (more && ok) {
           const int n = w.u1 - w.u0;
-          const bool two = w.it.n * p.group - w.it.rb * kA5R > 128;
+          const bool two = w.it.n - w.it.rb * tpb > p.tpt;
           const int nq = two ? 2 * n : n;
           ok = mbar_wait(&qfull[0], items & 1, 0x523) && mbar_wait(&qfull[1], items & 1, 0x524);
           auto qk = [&](int q) {
@@ -323,7 +362,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
           }
           tb += n;
           ++items;
-          more = w.next(a, p.group);
+          more = w.next(a, tpb);
         }
         t5_commit(done);                             // nothing in flight when tensor memory is freed
         mbar_wait(done, 0, 0x528);
@@ -335,32 +374,24 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
       const int tr = tid & 127;                      // row of the stream's tile = tensor-memory lane
       const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t ts = tl + s * 128, to = tl + 256 + s * D;
-      const uint32_t sq = sb + S::oQ + s * S::kTile;
-      int jt = 0, items = 0, jobs = 0;
+      const int tok = tr / p.group, head = tr - tok * p.group;   // in the row tile
+      int items = 0, jobs = 0;
       bool more = true;
       while (more) {
         const Item& it = w.it;
-        const int rows = it.n * p.group - it.rb * kA5R;          // of the item, maybe above 256
-        const bool two = rows > 128;
-        const int off = two ? s * 128 : 0;                       // first row of this stream in the item
+        const bool two = it.n - it.rb * tpb > p.tpt;
+        const int i0 = it.rb * tpb + (two ? s * p.tpt : 0);      // the row tile's first token
         const int n = w.u1 - w.u0;
-        const int shift = it.total - it.n;
-        // ---- Q: 16-byte chunks, rows beyond the item zero
-        for (int e = tr; e < 128 * (D / 8); e += 128) {
-          const int r = e / (D / 8), ch = e % (D / 8);
-          const int gr = it.rb * kA5R + off + r;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (off + r < rows)
-            v = ld_nc_v4(a.q + (long long)(it.start + gr / p.group) * a.q_stride + (long long)(it.h * p.group + gr % p.group) * D + 8 * ch);
-          a5_sts128(sq + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4), v);
+        if (tr == 0) {
+          a5_fence_proxy();                                      // Q's places held sums of the last item
+          mbar_arrive_expect_tx(&qfull[s], (uint32_t)(p.tpt * p.group * D * 2));
+#pragma unroll
+          for (int b = 0; b < D / 64; ++b)
+            a5_tma3(sb + S::oQ + s * S::kTile + b * 16384, &p.tq, 64 * b, it.h * p.group, it.start + i0, &qfull[s]);
         }
-        a5_fence_proxy();
-        t5_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&qfull[s]);
-        const int gr = it.rb * kA5R + off + tr;
-        const bool valid = off + tr < rows;
-        const int pos = shift + gr / p.group;
+        const int qi = i0 + tok;                                 // this row's token in the sequence
+        const bool valid = tok < p.tpt && qi < it.n;
+        const int pos = it.total - it.n + qi;
         // keys [rlo, rhi) that this row sees (rows beyond the item see all, and are not stored)
         const int rhi = !valid ? 0x7fffffff : pos < 0 ? 0 : a.causal ? min(it.total, pos + 1) : it.total;
         const int rlo = !valid ? 0 : a.window > 0 ? pos - a.window + 1 : 0;
@@ -368,8 +399,9 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         const int nj = two ? n : (n - s + 1) / 2;
         for (int q = 0; q < nj; ++q, ++jobs) {
           const int tile = two ? q : 2 * q + s;
-          const int slot = (jt + tile) & (kA5ScaleSlots - 1);
-          if (ok) ok = mbar_wait(&scfull[slot], ((jt + tile) / kA5ScaleSlots) & 1, 0x529);
+          const int jt = w.base + tile;
+          const int slot = jt & (kA5ScaleSlots - 1);
+          if (ok) ok = mbar_wait(&scfull[slot], (jt / kA5ScaleSlots) & 1, 0x529);
           if (ok) ok = mbar_wait(&sfull[s], jobs & 1, 0x52a);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -377,89 +409,102 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
           const int k0 = (it.t0 + w.u0 + tile) * kA5T;
           const uint32_t ssc = sb + S::oScales + slot * 128;
           const int clo = rlo - k0, chi = rhi - k0;              // columns that the row sees
+          // a warp whose rows all see the whole tile (nearly all of them) tests no key
           const bool masked = __any_sync(0xffffffffu, clo > 0 || chi < kA5T);
-          float mx = -INFINITY;
+          // O and the first `chunks` chunks of P over to a higher bound
+          auto raise = [&](float to_m, int chunks) {
+            const float al = to_m == m ? 1.f : attn_ex2(m - to_m);   // 0 where there was nothing
+            m = to_m;
+            l *= al;
+            a5_wait_st();
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float v[32];
-            a5_ld32(ts + c * 32, v);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float4 sc = a5_lds_f4(ssc + (c * 2 + h) * 16);
-              float x = -INFINITY;
+            for (int c = 0; c < (q > 0 ? D : 0); c += 32) {
+              float v[32];
+              a5_get32(to + c, v);
+              uint32_t r0[16], r1[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const int col = c * 32 + h * 16 + i;
-                const float y = !masked || (col >= clo && col < chi) ? v[h * 16 + i] : -INFINITY;
-                x = fmaxf(x, y);
+                r0[i] = __float_as_uint(v[i] * al);
+                r1[i] = __float_as_uint(v[16 + i] * al);
               }
-              mx = fmaxf(mx, x == -INFINITY ? x : fmaf(x, sc.x, sc.y));
+              a5_st16(to + c, r0);
+              a5_st16(to + c + 16, r1);
             }
-          }
-          const bool move = mx > m + kA5Slack;
-          if (__any_sync(0xffffffffu, move)) {
-            const float nm = move ? mx : m;
-            const float al = move ? attn_ex2(m - nm) : 1.f;      // 0 where there was nothing
-            m = nm;
-            l *= al;
-            if (q > 0) {
 #pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                float v[32];
-                a5_ld32(to + c, v);
-                uint32_t r0[16], r1[16];
+            for (int c = 0; c < chunks; ++c) {
+              float v[32];
+              a5_get32(ts + c * 16, v);                          // 16 columns of it are P
+              uint32_t r[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const uint32_t u = __float_as_uint(v[i]);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+                r[i] = a5_pack(f.x * al, f.y * al);
+              }
+              a5_st16(ts + c * 16, r);
+            }
+          };
+          auto pass = [&](auto test) {
+            float v[2][32];
+            a5_ld32(ts, v[0]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float (&x)[32] = v[c & 1];
+              a5_wait32(x);
+              if (c < 3) a5_ld32(ts + (c + 1) * 32, v[(c + 1) & 1]);
+              float4 sc[2];
+              float mx = -INFINITY;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                sc[h] = a5_lds_f4(ssc + (c * 2 + h) * 16);
+                float y = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                  r0[i] = __float_as_uint(v[i] * al);
-                  r1[i] = __float_as_uint(v[16 + i] * al);
+                  const int col = c * 32 + h * 16 + i;
+                  if (decltype(test)::value) x[h * 16 + i] = col >= clo && col < chi ? x[h * 16 + i] : -INFINITY;
+                  y = fmaxf(y, x[h * 16 + i]);
                 }
-                a5_st16(to + c, r0);
-                a5_st16(to + c + 16, r1);
+                mx = fmaxf(mx, y == -INFINITY ? y : fmaf(y, sc[h].x, sc[h].y));
               }
-            }
-          }
-          const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float v[32];
-            a5_ld32(ts + c * 32, v);
-            uint32_t pk[16];
+              if (__any_sync(0xffffffffu, mx > m + kA5Slack)) {
+                if (c < 3) a5_wait32(v[(c + 1) & 1]);
+                raise(mx > m + kA5Slack ? mx : m, c);
+              }
+              const float base = m == -INFINITY ? 0.f : m;
+              uint32_t pk[16];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float4 sc = a5_lds_f4(ssc + (c * 2 + h) * 16);
-              const float bb = sc.y - base;
-              float sum = 0.f;
+              for (int h = 0; h < 2; ++h) {
+                const float2 kk = make_float2(sc[h].x, sc[h].x), bb = make_float2(sc[h].y - base, sc[h].y - base);
+                float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                const int col = c * 32 + h * 16 + i;
-                float w0 = attn_ex2(fmaf(v[h * 16 + i], sc.x, bb)), w1 = attn_ex2(fmaf(v[h * 16 + i + 1], sc.x, bb));
-                if (masked) {
-                  w0 = col >= clo && col < chi ? w0 : 0.f;
-                  w1 = col + 1 >= clo && col + 1 < chi ? w1 : 0.f;
+                for (int i = 0; i < 16; i += 2) {
+                  const float2 e = a5_fma2(make_float2(x[h * 16 + i], x[h * 16 + i + 1]), kk, bb);
+                  const float2 y = make_float2(attn_ex2(e.x), attn_ex2(e.y));
+                  sum = a5_add2(sum, y);
+                  pk[h * 8 + i / 2] = a5_pack(y.x, y.y);
                 }
-                sum += w0 + w1;
-                pk[h * 8 + i / 2] = a5_pack(w0, w1);
+                l = fmaf(sum.x + sum.y, sc[h].z, l);
               }
-              l = fmaf(sum, sc.z, l);
+              a5_st16(ts + c * 16, pk);                          // over columns of S that have been read
             }
-            a5_st16(ts + c * 16, pk);                            // over columns of S that have been read
-          }
+          };
+          if (masked) pass(A5Flag<true>{}); else pass(A5Flag<false>{});
           a5_wait_st();
           t5_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&pfull[s]);
         }
-        jt += n;
         if (ok) ok = mbar_wait(&ofull[s], items & 1, 0x52b);
         ok = __all_sync(0xffffffffu, ok);
         t5_fence_after();
         ++items;
         // ---------------------------------------------------------------- the item's result
-        const bool whole = w.u0 == 0 && w.u1 == it.units;
-        const int c0 = sp.owner(w.at), c1 = sp.owner(w.at + it.units - 1);
+        const bool whole = w.whole();
+        const int c0 = w.first_cta(sp), c1 = w.last_cta(sp);
         float* slots = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.workspace) + kAttnMaxCtas * 4);
         constexpr size_t SLOT = attn_slot_floats(kA5R, D);
-        float* part = slots + SLOT * (2 * cta + (w.u0 == 0 ? 1 : 0));
+        const int off = two ? s * 128 : 0;
+        float* part = slots + SLOT * (2 * cta + (w.u0 == 0 ? 1 : 0)) + off + tr;
         // an item of one row tile: stream 1's sums come over through the (now idle) places of Q
         float* xo = reinterpret_cast<float*>(smem + S::oQ);
         float2* xml = reinterpret_cast<float2*>(smem + S::oMl);
@@ -472,7 +517,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
             for (int c = 0; c < D; c += 32) {
               float v[32];
               if (nj > 0) {
-                a5_ld32(to + c, v);
+                a5_get32(to + c, v);
               } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = 0.f;
@@ -493,26 +538,26 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
           }
         }
         const bool mine = two || s == 0;                         // this stream writes rows
-        const bool some = l > 0.f || l != l;
-        const float inv = some ? __fdiv_rn(1.f, l) : 0.f;
+        const int orow = it.h * p.group + head;
+        __half* dst = a.out + (long long)(it.start + qi) * a.out_stride + (long long)orow * D;
         auto put = [&](int c, const float (&v)[32], float scale) {
-          __half* dst = a.out + (long long)(it.start + gr / p.group) * a.out_stride + (long long)(it.h * p.group + gr % p.group) * D + c;
 #pragma unroll
           for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(dst + i) =
+            *reinterpret_cast<uint4*>(dst + c + i) =
                 make_uint4(a5_pack(v[i] * scale, v[i + 1] * scale), a5_pack(v[i + 2] * scale, v[i + 3] * scale),
                            a5_pack(v[i + 4] * scale, v[i + 5] * scale), a5_pack(v[i + 6] * scale, v[i + 7] * scale));
         };
         auto put_lse = [&](float mm, float ll) {
           if (a.lse)
-            a.lse[(long long)(it.start + gr / p.group) * a.q_heads + it.h * p.group + gr % p.group] =
+            a.lse[(long long)(it.start + qi) * a.q_heads + orow] =
                 ll > 0.f || ll != ll ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
         };
         if (mine) {
+          const float inv = l > 0.f || l != l ? __fdiv_rn(1.f, l) : 0.f;
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float v[32];
-            a5_ld32(to + c, v);
+            a5_get32(to + c, v);
             if (!two) {
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
@@ -526,18 +571,16 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
             if (whole) {
               if (valid) put(c, v, inv);
             } else {
-              // [channel / 4][row]: a warp's stores are contiguous
+              // [channel][row]: a warp's stores are contiguous
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4*>(part + ((size_t)((c + i) / 4) * kA5R + off + tr) * 4) =
-                    make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+              for (int i = 0; i < 32; ++i) part[(size_t)(c + i) * kA5R] = v[i];
             }
           }
           if (whole) {
             if (valid) put_lse(m, l);
           } else {
-            part[(size_t)kA5R * D + off + tr] = m;
-            part[(size_t)kA5R * D + kA5R + off + tr] = l;
+            part[(size_t)kA5R * D] = m;
+            part[(size_t)kA5R * (D + 1)] = l;
           }
         }
         if (!whole) {
@@ -549,31 +592,27 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
           a5_sync_softmax();
           if (*flag && mine && valid) {
             __threadfence();
+            auto piece = [&](int c) { return slots + SLOT * (2 * c + (c == c0 ? 1 : 0)) + off + tr; };
             float mm = -INFINITY, ll = 0.f;
-            for (int c = c0; c <= c1; ++c)
-              mm = fmaxf(mm, __ldcg(slots + SLOT * (2 * c + (c == c0 ? 1 : 0)) + (size_t)kA5R * D + off + tr));
+            for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, __ldcg(piece(c) + (size_t)kA5R * D));
             const float b = mm == -INFINITY ? 0.f : mm;
-            for (int c = c0; c <= c1; ++c) {
-              const float* x = slots + SLOT * (2 * c + (c == c0 ? 1 : 0)) + (size_t)kA5R * D + off + tr;
-              ll = fmaf(__ldcg(x + kA5R), attn_ex2(__ldcg(x) - b), ll);
-            }
+            for (int c = c0; c <= c1; ++c)
+              ll = fmaf(__ldcg(piece(c) + (size_t)kA5R * (D + 1)), attn_ex2(__ldcg(piece(c) + (size_t)kA5R * D) - b), ll);
             const float iv = ll > 0.f || ll != ll ? __fdiv_rn(1.f, ll) : 0.f;
 #pragma unroll 1
             for (int ch = 0; ch < D; ch += 32) {
               float v[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = 0.f;
+#pragma unroll 1
               for (int c = c0; c <= c1; ++c) {
-                const float* x = slots + SLOT * (2 * c + (c == c0 ? 1 : 0));
-                const float f = attn_ex2(__ldcg(x + (size_t)kA5R * D + off + tr) - b);
+                const float* x = piece(c);
+                float y[32];
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  const float4 y = __ldcg(reinterpret_cast<const float4*>(x + ((size_t)((ch + i) / 4) * kA5R + off + tr) * 4));
-                  v[i] = fmaf(y.x, f, v[i]);
-                  v[i + 1] = fmaf(y.y, f, v[i + 1]);
-                  v[i + 2] = fmaf(y.z, f, v[i + 2]);
-                  v[i + 3] = fmaf(y.w, f, v[i + 3]);
-                }
+                for (int i = 0; i < 32; ++i) y[i] = __ldcg(x + (size_t)(ch + i) * kA5R);
+                const float f = attn_ex2(__ldcg(x + (size_t)kA5R * D) - b);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = fmaf(y[i], f, v[i]);
               }
               put(ch, v, iv);
             }
@@ -584,13 +623,13 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         if (!ok && lane == 0) *reinterpret_cast<volatile int*>(bad) = 1;
         a5_sync_softmax();                                       // Q's places and the flag are free again
         if (*reinterpret_cast<volatile int*>(bad)) break;
-        more = w.next(a, p.group);
+        more = w.next(a, tpb);
       }
     }
   }
   t5_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == kA5Mma) {
     t5_fence_after();
     t5_free512(tmem);
   }
@@ -625,8 +664,8 @@ cudaError_t launch_attn5(const AttnArgs& a, cudaStream_t stream) {
   A5Params p;
   p.a = a;
   p.group = a.q_heads / a.c.kv_heads;
-  p.max_blocks = (a.max_q * p.group + kA5R - 1) / kA5R;
-  p.min_units = 4;
+  p.tpt = 128 / p.group;
+  if (!encode_tmap_rows(&p.tq, a.q, a.c.dim, a.q_heads, a.tokens, a.q_stride, p.group, p.tpt)) return cudaErrorNotSupported;
   return a.c.dim == 128 ? launch_attn5_d<128>(p, stream) : launch_attn5_d<64>(p, stream);
 }
 

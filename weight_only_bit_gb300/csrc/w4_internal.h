@@ -75,6 +75,11 @@ bool encode_tmap_2d(CUtensorMap* m, int es, const void* base, long long cols, lo
 bool encode_tmap_pages(CUtensorMap* m, const void* base, int dim, long long rows, long long pages, long long page_stride,
                        int box_rows);
 
+// 3-D tiled TMA map over FP16 rows [tokens][heads][dim] with `row_stride` elements from a token to the
+// next: box of box_tokens x box_heads rows of 64 elements, 128-byte swizzle, zeros outside the array.
+bool encode_tmap_rows(CUtensorMap* m, const void* base, int dim, long long heads, long long tokens, long long row_stride,
+                      int box_heads, int box_tokens);
+
 // Keeps the error for w4_last_cuda_error() and returns the w4_status that stands for it.
 int cuda_status(cudaError_t e);
 
