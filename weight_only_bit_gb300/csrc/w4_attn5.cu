@@ -13,7 +13,8 @@
 // end; so the two softmax warpgroups always overlap the other's products.
 // Tensor memory is full: S 2 x 128 columns, O 2 x D columns (256 at D = 128); the weights P go back
 // over the first half of their S as FP16, the A operand of the second product.
-// Roles (13 warps, so that a thread may hold 128 registers), connected by mbarriers:
+// Roles (four warpgroups of 128 threads; registers move from the last to the first two), connected by
+// mbarriers:
 //   warps 0-3, 4-7   softmax of stream 0 and 1: a thread per row, one pass over its S: 32 keys at a time,
 //                    their maximum, then weights, sums, P.  Where a maximum passes the bound (the
 //                    first keys of an item, rarely later), O and the P written so far are rescaled in
@@ -21,7 +22,8 @@
 //   warps 8-11       codes from global memory, FP16 into shared memory: keys in the canonical K-major
 //                    layout, values in the MN-major one (channels contiguous, as they lie in
 //                    memory: nothing is transposed).  A tile's loads are issued a tile ahead.
-//   warp 12          issues the MMAs: PV of a stream, then its next S, alternating between streams
+//   warp 12          issues the MMAs: PV of a stream, then its next S, alternating between streams (the
+//                    whole warp walks, one elected lane issues: descriptors stay in uniform registers)
 // What bounds it: figures beside the launch below.
 #include <cstdint>
 #include <cuda.h>
@@ -40,7 +42,9 @@ constexpr int kA5T = 128;                    // keys per tile
 constexpr int kA5R = 256;                    // rows per item, at most
 constexpr int kA5Ov = 2;                     // what an item costs beside its tiles
 constexpr int kA5Mma = 12;                   // the issuing warp
-constexpr int kA5Threads = (kA5Mma + 1) * 32;
+constexpr int kA5Threads = 512;
+// Registers a thread: launched with 128 each (65536 in all); 2 x 128 x 168 + 128 x 128 + 128 x 48 = 65536.
+constexpr int kA5RegsSoftmax = 168, kA5RegsMma = 48;
 constexpr float kA5Slack = 6.f;
 constexpr int kA5ScaleSlots = 4;
 
@@ -146,6 +150,35 @@ __device__ __forceinline__ void a5_tma3(uint32_t dst, const CUtensorMap* map, in
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)) : "memory");
 }
 
+// One lane of the (whole) warp: 1 in it, 0 in the others.
+__device__ __forceinline__ uint32_t a5_elect() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+  return e;
+}
+// The MMA and commit of the shared header, predicated on the elected lane (no branch: the operands
+// stay warp-uniform).
+__device__ __forceinline__ void a5_mma_ss(uint32_t lead, uint32_t dtmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+      ::"r"(dtmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void a5_mma_ts(uint32_t lead, uint32_t dtmem, uint32_t atmem, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+      ::"r"(dtmem), "r"(atmem), "l"(bdesc), "r"(idesc), "r"(acc), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void a5_commit(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
+      ::"r"(smem_u32(bar)), "r"(lead) : "memory");
+}
+
 // Two FP32 operations in one instruction.
 __device__ __forceinline__ float2 a5_fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -240,7 +273,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         return page;
       };
       uint4 dk[NP], dv[NP];
-      float4 sc = make_float4(1.f, 0.f, 1.f, 0.f);
+      float ks = 1.f, vs = 1.f;                      // of lane < 2's group
       // issues the loads of the tile at (w, u), its scales too
       auto load = [&](int page) {
         const int k0 = (w.it.t0 + u) * kA5T + wq * 32;
@@ -258,12 +291,10 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
             dv[i] = ld_nc_v4(a.c.v + at);
           }
         }
-        sc = make_float4(1.f, 0.f, 1.f, 0.f);
+        ks = vs = 1.f;
         if (lane < 2 && page >= 0) {
-          sc.x = __ldg(a.c.k_scale + (long long)page * a.c.scale_stride + w.it.h) * c2;
-          const float vs = __ldg(a.c.v_scale + (long long)page * a.c.scale_stride + w.it.h);
-          sc.y = log2f(vs);
-          sc.z = __fdiv_rn(1.f, vs);
+          ks = __ldg(a.c.k_scale + (long long)page * a.c.scale_stride + w.it.h);
+          vs = __ldg(a.c.v_scale + (long long)page * a.c.scale_stride + w.it.h);
         }
       };
       // 16-byte chunks 2 (l % 4) and the next of the row's 128 bytes; half of the lanes begin with the
@@ -282,13 +313,16 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
           a5_sts128(row + ((cb ^ r) << 4), second ? x0 : x1);
         }
       };
-      load(pages_of(true));
-      while (more && ok) {
-        // the next tile's pages, while this one's data are on their way
+      auto advance = [&] {
         if (++u >= w.u1) {
           more = w.next(a, tpb);
           u = w.u0;
         }
+      };
+      load(pages_of(true));
+      while (more && ok) {
+        // the next tile's pages, while this one's data are on their way
+        advance();
         const int page = pages_of(more);
         const int st = j & 1;
         if (j >= 2) ok = mbar_wait(&kempty[st], ((j >> 1) - 1) & 1, 0x521);
@@ -296,7 +330,8 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         if (!ok) break;
         decode(sb + S::oK + st * S::kTile, dk);
         if (lane < 2)
-          *reinterpret_cast<float4*>(smem + S::oScales + ((j & (kA5ScaleSlots - 1)) * 8 + wq * 2 + lane) * 16) = sc;
+          *reinterpret_cast<float4*>(smem + S::oScales + ((j & (kA5ScaleSlots - 1)) * 8 + wq * 2 + lane) * 16) =
+              make_float4(ks * c2, log2f(vs), __fdiv_rn(1.f, vs), 0.f);
         a5_fence_proxy();
         __syncwarp();
         if (lane == 0) {
@@ -313,63 +348,68 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         ++j;
         if (more) load(page);
       }
-    } else if (warp == kA5Mma) {
+    } else if (warp >= kA5Mma) {
       // ================================================================ MMA issuer
-      if (lane == 0) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kA5RegsMma));
+      if (warp == kA5Mma) {
         constexpr uint32_t id_s = a5_idesc(128, false), id_o = a5_idesc(D, true);
-        int tb = 0, items = 0;                       // tiles and items before this one
+        const uint32_t lead = a5_elect();
+        const uint64_t dq = a5_desc_k(sb + S::oQ), dk = a5_desc_k(sb + S::oK), dv = a5_desc_mn(sb + S::oV);
+        constexpr uint64_t kStep = S::kTile >> 4;    // from a stage, or a stream's q, to the next
+        int items = 0;
         int jobs[2] = {0, 0};                        // jobs of each stream so far
         bool more = true;
         while (more && ok) {
-          const int n = w.u1 - w.u0;
+          const int n = w.u1 - w.u0, tb = w.base;
           const bool two = w.it.n - w.it.rb * tpb > p.tpt;
           const int nq = two ? 2 * n : n;
           ok = mbar_wait(&qfull[0], items & 1, 0x523) && mbar_wait(&qfull[1], items & 1, 0x524);
           auto qk = [&](int q) {
             const int s = q & 1, tile = tb + (two ? q >> 1 : q);
             if (!two || s == 0) ok = ok && mbar_wait(&kfull[tile & 1], (tile >> 1) & 1, 0x525);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
             t5_fence_after();
-            const uint32_t qa = sb + S::oQ + s * S::kTile, ka = sb + S::oK + (tile & 1) * S::kTile;
+            const uint64_t qa = dq + s * kStep, ka = dk + (tile & 1) * kStep;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-              t5_mma_ss(tmem + s * 128, a5_desc_k(qa + off), a5_desc_k(ka + off), id_s, k > 0 ? 1u : 0u);
+              const uint64_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+              a5_mma_ss(lead, tmem + s * 128, qa + off, ka + off, id_s, k > 0 ? 1u : 0u);
             }
-            t5_commit(&sfull[s]);
-            if (!two || s == 1) t5_commit(&kempty[tile & 1]);
+            a5_commit(lead, &sfull[s]);
+            if (!two || s == 1) a5_commit(lead, &kempty[tile & 1]);
           };
           auto pv = [&](int q) {
             const int s = q & 1, tile = tb + (two ? q >> 1 : q);
             if (!two || s == 0) ok = ok && mbar_wait(&vfull[tile & 1], (tile >> 1) & 1, 0x526);
             ok = ok && mbar_wait(&pfull[s], jobs[s] & 1, 0x527);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
             ++jobs[s];
             t5_fence_after();
-            const uint32_t va = sb + S::oV + (tile & 1) * S::kTile;
+            const uint64_t va = dv + (tile & 1) * kStep;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              t5_mma_ts(tmem + 256 + s * D, tmem + s * 128 + k * 8, a5_desc_mn(va + k * 2048), id_o, (q >= 2 || k > 0) ? 1u : 0u);
-            if (!two || s == 1) t5_commit(&vempty[tile & 1]);
-            if (q + 2 >= nq) t5_commit(&ofull[s]);
+              a5_mma_ts(lead, tmem + 256 + s * D, tmem + s * 128 + k * 8, va + ((k * 2048) >> 4), id_o, (q >= 2 || k > 0) ? 1u : 0u);
+            if (!two || s == 1) a5_commit(lead, &vempty[tile & 1]);
+            if (q + 2 >= nq) a5_commit(lead, &ofull[s]);
           };
           if (ok) qk(0);
           if (ok && nq > 1) qk(1);
-          if (ok && nq == 1) t5_commit(&ofull[1]);   // the other stream has no tile
+          if (ok && nq == 1) a5_commit(lead, &ofull[1]);   // the other stream has no tile
           for (int q = 0; q < nq && ok; ++q) {
             pv(q);
             if (ok && q + 2 < nq) qk(q + 2);
           }
-          tb += n;
           ++items;
           more = w.next(a, tpb);
         }
-        t5_commit(done);                             // nothing in flight when tensor memory is freed
+        a5_commit(lead, done);                       // nothing in flight when tensor memory is freed
         mbar_wait(done, 0, 0x528);
       }
-      __syncwarp();
-    } else if (warp < 8) {
+    } else {
       // ================================================================ softmax
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kA5RegsSoftmax));
       const int s = warp >> 2;
       const int tr = tid & 127;                      // row of the stream's tile = tensor-memory lane
       const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
