@@ -65,7 +65,8 @@ struct A5Smem {
   static constexpr int kBars = 2 + 2 + 2 + 2 + kA5ScaleSlots + 2 + 2 + 2 + 2 + 1;
   static constexpr int oFlag = oBar + kBars * 8;
   static constexpr int oPrefix = oFlag + 16;
-  static constexpr int kTotal = oPrefix + (W4_MAX_SEQS + 1) * 4 + 1024;
+  static constexpr int oOut = (oPrefix + (W4_MAX_SEQS + 1) * 4 + 15) & ~15;   // 8 softmax warps x 32 rows x 64 bytes
+  static constexpr int kTotal = oOut + 8 * 2048 + 1024;
 };
 
 struct A5Params {
@@ -250,10 +251,12 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
     if (warp >= 8 && warp < kA5Mma) {
       // ================================================================ keys and values into shared memory
       const int wq = warp & 3;                       // rows 32 wq ... + 31 of the tile
-      constexpr int LPR = D / 16;                    // lanes per row
-      constexpr int RPI = 32 / LPR;                  // rows per pass of the warp
+      constexpr int RPI = 512 / D;                   // rows per pass of the warp (16 codes a lane)
       constexpr int NP = 32 / RPI;                   // passes
-      const int l = lane % LPR, rl = lane / LPR;
+      // lane -> row of the pass, 64-channel block, 16 channels of it.  A quarter-warp covers four 16-channel
+      // pieces of an even row and the next one, so that its 16-byte stores meet all banks once under the swizzle.
+      const int rl = D == 128 ? (lane >> 4) * 2 + ((lane >> 2) & 1) : lane >> 2;
+      const int blk = D == 128 ? (lane >> 3) & 1 : 0, l4 = lane & 3;
       const int P = a.c.page;
       int u = w.u0, j = 0;
       bool more = true;
@@ -277,18 +280,23 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
       // issues the loads of the tile at (w, u), its scales too
       auto load = [&](int page) {
         const int k0 = (w.it.t0 + u) * kA5T + wq * 32;
-        const int pg0 = __shfl_sync(0xffffffffu, page, 0), pg1 = __shfl_sync(0xffffffffu, page, 1);
+        const long long at = (long long)((k0 + rl) & (P - 1)) * D + (long long)w.it.h * P * D + blk * 64 + 16 * l4;
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const int r = i * RPI + rl;
-          const int key = k0 + r;
-          const int pg = r < 16 ? pg0 : pg1;
-          // rows that nobody sees are zero: their weights are 0, and 0 times a stale NaN would not be
-          dk[i] = dv[i] = make_uint4(0, 0, 0, 0);
-          if (pg >= 0 && key >= w.it.lo && key < w.it.hi) {
-            const long long at = (long long)pg * a.c.page_stride + (long long)(w.it.h * P + (key & (P - 1))) * D + 16 * l;
-            dk[i] = ld_nc_v4(a.c.k + at);
-            dv[i] = ld_nc_v4(a.c.v + at);
+        for (int g = 0; g < 2; ++g) {                // 16-key groups: one page each
+          const int pg = __shfl_sync(0xffffffffu, page, g);
+          // a page of 16 rows begins again with each group
+          const long long off = (long long)pg * a.c.page_stride + at + (P > 16 ? g * 16 * D : 0);
+          const uint8_t* ks_ = a.c.k + off;
+          const uint8_t* vs_ = a.c.v + off;
+#pragma unroll
+          for (int i = 0; i < NP / 2; ++i) {
+            const int key = k0 + g * 16 + i * RPI + rl, x = g * (NP / 2) + i;
+            // rows that nobody sees are zero: their weights are 0, and 0 times a stale NaN would not be
+            dk[x] = dv[x] = make_uint4(0, 0, 0, 0);
+            if (pg >= 0 && key >= w.it.lo && key < w.it.hi) {
+              dk[x] = ld_nc_v4(ks_ + i * RPI * D);
+              dv[x] = ld_nc_v4(vs_ + i * RPI * D);
+            }
           }
         }
         ks = vs = 1.f;
@@ -297,11 +305,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
           vs = __ldg(a.c.v_scale + (long long)page * a.c.scale_stride + w.it.h);
         }
       };
-      // 16-byte chunks 2 (l % 4) and the next of the row's 128 bytes; half of the lanes begin with the
-      // second, so that a quarter-warp's stores meet all banks once
-      const bool second = (l >> 2) & 1;
-      const uint32_t ca = 2 * (l & 3) + (second ? 1 : 0), cb = ca ^ 1;
-      const uint32_t at = (uint32_t)(l >> 2) * 16384 + (uint32_t)(wq * 32 + rl) * 128;
+      const uint32_t at = (uint32_t)blk * 16384 + (uint32_t)(wq * 32 + rl) * 128;
       auto decode = [&](uint32_t base, const uint4 (&d)[NP]) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
@@ -309,8 +313,8 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
           uint4 x0, x1;
           a5_cvt16(d[i], x0, x1);
           const uint32_t row = base + at + i * RPI * 128;
-          a5_sts128(row + ((ca ^ r) << 4), second ? x1 : x0);
-          a5_sts128(row + ((cb ^ r) << 4), second ? x0 : x1);
+          a5_sts128(row + (((2 * l4) ^ r) << 4), x0);
+          a5_sts128(row + (((2 * l4 + 1) ^ r) << 4), x1);
         }
       };
       auto advance = [&] {
@@ -416,19 +420,24 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
       const uint32_t ts = tl + s * 128, to = tl + 256 + s * D;
       const int tok = tr / p.group, head = tr - tok * p.group;   // in the row tile
       int items = 0, jobs = 0;
-      bool more = true;
+      bool more = true, asked = false;               // asked: this item's q is on its way
+      auto ask_q = [&](const Item& x) {
+        if (tr == 0) {
+          a5_fence_proxy();                                      // the places may have held sums of an item
+          mbar_arrive_expect_tx(&qfull[s], (uint32_t)(p.tpt * p.group * D * 2));
+          const int t0 = x.start + x.rb * tpb + (x.n - x.rb * tpb > p.tpt ? s * p.tpt : 0);
+#pragma unroll
+          for (int b = 0; b < D / 64; ++b)
+            a5_tma3(sb + S::oQ + s * S::kTile + b * 16384, &p.tq, 64 * b, x.h * p.group, t0, &qfull[s]);
+        }
+      };
       while (more) {
         const Item& it = w.it;
         const bool two = it.n - it.rb * tpb > p.tpt;
         const int i0 = it.rb * tpb + (two ? s * p.tpt : 0);      // the row tile's first token
         const int n = w.u1 - w.u0;
-        if (tr == 0) {
-          a5_fence_proxy();                                      // Q's places held sums of the last item
-          mbar_arrive_expect_tx(&qfull[s], (uint32_t)(p.tpt * p.group * D * 2));
-#pragma unroll
-          for (int b = 0; b < D / 64; ++b)
-            a5_tma3(sb + S::oQ + s * S::kTile + b * 16384, &p.tq, 64 * b, it.h * p.group, it.start + i0, &qfull[s]);
-        }
+        if (!asked) ask_q(w.it);
+        asked = false;
         const int qi = i0 + tok;                                 // this row's token in the sequence
         const bool valid = tok < p.tpt && qi < it.n;
         const int pos = it.total - it.n + qi;
@@ -446,6 +455,14 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           t5_fence_after();
+          if (two && q == nj - 1) {
+            // the item's products with q are complete: the next item's rows may come in
+            Walk<kA5T, kA5Ov> nx = w;
+            if (nx.next(a, tpb)) {
+              ask_q(nx.it);
+              asked = true;
+            }
+          }
           const int k0 = (it.t0 + w.u0 + tile) * kA5T;
           const uint32_t ssc = sb + S::oScales + slot * 128;
           const int clo = rlo - k0, chi = rhi - k0;              // columns that the row sees
@@ -484,37 +501,53 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
               a5_st16(ts + c * 16, r);
             }
           };
+          // Chunks of 32 keys, three in flight: the weights of one, the maximum of the next, the load of
+          // the one after.
           auto pass = [&](auto test) {
-            float v[2][32];
-            a5_ld32(ts, v[0]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float (&x)[32] = v[c & 1];
+            float v[3][32];
+            auto look = [&](int c) {                             // the chunk's maximum against the bound
+              float (&x)[32] = v[c % 3];
               a5_wait32(x);
-              if (c < 3) a5_ld32(ts + (c + 1) * 32, v[(c + 1) & 1]);
-              float4 sc[2];
+              if (c < 3) a5_ld32(ts + (c + 1) * 32, v[(c + 1) % 3]);
               float mx = -INFINITY;
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                sc[h] = a5_lds_f4(ssc + (c * 2 + h) * 16);
-                float y = -INFINITY;
+                const float4 sc = a5_lds_f4(ssc + (c * 2 + h) * 16);
+                if (decltype(test)::value) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const int col = c * 32 + h * 16 + i;
-                  if (decltype(test)::value) x[h * 16 + i] = col >= clo && col < chi ? x[h * 16 + i] : -INFINITY;
-                  y = fmaxf(y, x[h * 16 + i]);
+                  for (int i = 0; i < 16; ++i) {
+                    const int col = c * 32 + h * 16 + i;
+                    x[h * 16 + i] = col >= clo && col < chi ? x[h * 16 + i] : -INFINITY;
+                  }
                 }
-                mx = fmaxf(mx, y == -INFINITY ? y : fmaf(y, sc[h].x, sc[h].y));
+                float y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  y[i] = fmaxf(fmaxf(x[h * 16 + i], x[h * 16 + 4 + i]), fmaxf(x[h * 16 + 8 + i], x[h * 16 + 12 + i]));
+                const float z = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+                mx = fmaxf(mx, z == -INFINITY ? z : fmaf(z, sc.x, sc.y));
               }
+              return mx;
+            };
+            auto settle = [&](float mx, int c, int written) {    // c: the chunk of mx; `written` chunks are P
               if (__any_sync(0xffffffffu, mx > m + kA5Slack)) {
-                if (c < 3) a5_wait32(v[(c + 1) & 1]);
-                raise(mx > m + kA5Slack ? mx : m, c);
+                if (c < 3) a5_wait32(v[(c + 1) % 3]);
+                raise(mx > m + kA5Slack ? mx : m, written);
               }
+            };
+            a5_ld32(ts, v[0]);
+            settle(look(0), 0, 0);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float nx = -INFINITY;
+              if (c < 3) nx = look(c + 1);
+              float (&x)[32] = v[c % 3];
               const float base = m == -INFINITY ? 0.f : m;
               uint32_t pk[16];
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const float2 kk = make_float2(sc[h].x, sc[h].x), bb = make_float2(sc[h].y - base, sc[h].y - base);
+                const float4 sc = a5_lds_f4(ssc + (c * 2 + h) * 16);
+                const float2 kk = make_float2(sc.x, sc.x), bb = make_float2(sc.y - base, sc.y - base);
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
@@ -523,9 +556,10 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
                   sum = a5_add2(sum, y);
                   pk[h * 8 + i / 2] = a5_pack(y.x, y.y);
                 }
-                l = fmaf(sum.x + sum.y, sc[h].z, l);
+                l = fmaf(sum.x + sum.y, sc.z, l);
               }
               a5_st16(ts + c * 16, pk);                          // over columns of S that have been read
+              if (c < 3) settle(nx, c + 1, c + 1);
             }
           };
           if (masked) pass(A5Flag<true>{}); else pass(A5Flag<false>{});
@@ -580,12 +614,24 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         const bool mine = two || s == 0;                         // this stream writes rows
         const int orow = it.h * p.group + head;
         __half* dst = a.out + (long long)(it.start + qi) * a.out_stride + (long long)orow * D;
+        // 32 channels of the warp's rows: through shared memory, so that a store covers 64 bytes of 8 rows
+        // (16 bytes of 32 rows would be twice the sectors and four times the lines).  By the whole warp.
+        const uint32_t stage = sb + S::oOut + warp * 2048;
         auto put = [&](int c, const float (&v)[32], float scale) {
+          __syncwarp();
 #pragma unroll
           for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(dst + c + i) =
-                make_uint4(a5_pack(v[i] * scale, v[i + 1] * scale), a5_pack(v[i + 2] * scale, v[i + 3] * scale),
-                           a5_pack(v[i + 4] * scale, v[i + 5] * scale), a5_pack(v[i + 6] * scale, v[i + 7] * scale));
+            a5_sts128(stage + lane * 64 + (((i / 8) ^ ((lane >> 1) & 3)) << 4),
+                      make_uint4(a5_pack(v[i] * scale, v[i + 1] * scale), a5_pack(v[i + 2] * scale, v[i + 3] * scale),
+                                 a5_pack(v[i + 4] * scale, v[i + 5] * scale), a5_pack(v[i + 6] * scale, v[i + 7] * scale)));
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = k * 8 + (lane >> 2);
+            const float4 x = a5_lds_f4(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+            __half* d = reinterpret_cast<__half*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(valid ? dst : nullptr), r));
+            if (d) *reinterpret_cast<float4*>(d + c + 8 * (lane & 3)) = x;
+          }
         };
         auto put_lse = [&](float mm, float ll) {
           if (a.lse)
@@ -609,7 +655,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
               }
             }
             if (whole) {
-              if (valid) put(c, v, inv);
+              put(c, v, inv);
             } else {
               // [channel][row]: a warp's stores are contiguous
 #pragma unroll
@@ -630,7 +676,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
           a5_sync_softmax();
           if (tid == 0) *flag = atomicAdd(ticket, 1u) == (unsigned)(c1 - c0);
           a5_sync_softmax();
-          if (*flag && mine && valid) {
+          if (*flag && mine) {
             __threadfence();
             auto piece = [&](int c) { return slots + SLOT * (2 * c + (c == c0 ? 1 : 0)) + off + tr; };
             float mm = -INFINITY, ll = 0.f;
@@ -656,7 +702,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
               }
               put(ch, v, iv);
             }
-            put_lse(mm, ll);
+            if (valid) put_lse(mm, ll);
           }
           if (*flag && tid == 0) *ticket = 0;
         }
