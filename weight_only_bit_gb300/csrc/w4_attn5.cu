@@ -12,13 +12,14 @@
 // of one row tile gives both streams the same rows and every second key tile each, joined at the
 // end; so the two softmax warpgroups always overlap the other's products.
 // Tensor memory is full: S 2 x 128 columns, O 2 x D columns (256 at D = 128); the weights P go back
-// over the first half of their S as FP16, the A operand of the second product.
+// over the first half of their S as FP16, the A operand of the second product.  A stream's S is two
+// halves of 64 keys with barriers of their own: while the softmax warps turn one half into weights, the
+// tensor cores multiply the other half's weights and fill it again.
 // Roles (four warpgroups of 128 threads; registers move from the last to the first two), connected by
 // mbarriers:
-//   warps 0-3, 4-7   softmax of stream 0 and 1: a thread per row, one pass over its S: 32 keys at a time,
+//   warps 0-3, 4-7   softmax of stream 0 and 1: a thread per row, one pass over its S, 64 keys at a time:
 //                    their maximum, then weights, sums, P.  Where a maximum passes the bound (the
-//                    first keys of an item, rarely later), O and the P written so far are rescaled in
-//                    place.  At the end out.
+//                    first keys of an item, rarely later), O is rescaled in place.  At the end out.
 //   warps 8-11       codes from global memory, FP16 into shared memory: keys in the canonical K-major
 //                    layout, values in the MN-major one (channels contiguous, as they lie in
 //                    memory: nothing is transposed).  A tile's loads are issued a tile ahead.
@@ -48,11 +49,6 @@ constexpr int kA5RegsSoftmax = 168, kA5RegsMma = 48;
 constexpr float kA5Slack = 6.f;
 constexpr int kA5ScaleSlots = 4;
 
-template <bool B>
-struct A5Flag {
-  static constexpr bool value = B;
-};
-
 template <int D>
 struct A5Smem {
   static constexpr int kTile = 128 * D * 2;              // 128 rows of FP16: D / 64 blocks of 128 x 128 bytes
@@ -62,7 +58,7 @@ struct A5Smem {
   static constexpr int oScales = 6 * kTile;              // [slots][8 groups] (ks c, log2 vs, 1 / vs, 0)
   static constexpr int oMl = oScales + kA5ScaleSlots * 8 * 16;   // [128] (maximum, sum) of stream 1
   static constexpr int oBar = oMl + 128 * 8;
-  static constexpr int kBars = 2 + 2 + 2 + 2 + kA5ScaleSlots + 2 + 2 + 2 + 2 + 1;
+  static constexpr int kBars = 2 + 2 + 2 + 2 + kA5ScaleSlots + 4 + 4 + 2 + 4 + 1;
   static constexpr int oFlag = oBar + kBars * 8;
   static constexpr int oPrefix = oFlag + 16;
   static constexpr int oOut = (oPrefix + (W4_MAX_SEQS + 1) * 4 + 15) & ~15;   // 8 softmax warps x 32 rows x 64 bytes
@@ -180,6 +176,12 @@ __device__ __forceinline__ void a5_commit(uint32_t lead, uint64_t* bar) {
       ::"r"(smem_u32(bar)), "r"(lead) : "memory");
 }
 
+__device__ __forceinline__ float a5_max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Two FP32 operations in one instruction.
 __device__ __forceinline__ float2 a5_fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -206,11 +208,11 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
   uint64_t* vfull = kempty + 2;
   uint64_t* vempty = vfull + 2;
   uint64_t* scfull = vempty + 2;                                  // 4 decoding warps
-  uint64_t* sfull = scfull + kA5ScaleSlots;                       // commit: S of the stream is there
-  uint64_t* pfull = sfull + 2;                                    // 4 softmax warps: P of the stream is there
-  uint64_t* qfull = pfull + 2;                                    // TMA: Q of the stream is there
-  uint64_t* ofull = qfull + 2;                                    // commit: O of the stream is complete
-  uint64_t* done = ofull + 2;
+  uint64_t* sfull = scfull + kA5ScaleSlots;                       // commit: S of (stream, half) is there
+  uint64_t* pfull = sfull + 4;                                    // 4 softmax warps: P of (stream, half) is there
+  uint64_t* qfull = pfull + 4;                                    // TMA: Q of the stream is there
+  uint64_t* pvdone = qfull + 2;                                   // commit: O has taken in P of (stream, half)
+  uint64_t* done = pvdone + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::oFlag);
   int* flag = reinterpret_cast<int*>(smem + S::oFlag + 8);
   int* bad = flag + 1;                       // a softmax warp lost a wait: all of them leave together
@@ -223,10 +225,12 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
       mbar_init(&kempty[i], 1);
       mbar_init(&vfull[i], 4);
       mbar_init(&vempty[i], 1);
+      mbar_init(&qfull[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], 4);
-      mbar_init(&qfull[i], 1);
-      mbar_init(&ofull[i], 1);
+      mbar_init(&pvdone[i], 1);
     }
     for (int i = 0; i < kA5ScaleSlots; ++i) mbar_init(&scfull[i], 4);
     mbar_init(done, 1);
@@ -356,54 +360,56 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
       // ================================================================ MMA issuer
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kA5RegsMma));
       if (warp == kA5Mma) {
-        constexpr uint32_t id_s = a5_idesc(128, false), id_o = a5_idesc(D, true);
+        constexpr uint32_t id_s = a5_idesc(64, false), id_o = a5_idesc(D, true);
         const uint32_t lead = a5_elect();
         const uint64_t dq = a5_desc_k(sb + S::oQ), dk = a5_desc_k(sb + S::oK), dv = a5_desc_mn(sb + S::oV);
         constexpr uint64_t kStep = S::kTile >> 4;    // from a stage, or a stream's q, to the next
         int items = 0;
-        int jobs[2] = {0, 0};                        // jobs of each stream so far
+        uint32_t turn = 0;                           // parity of pfull, a bit per stream
         bool more = true;
         while (more && ok) {
           const int n = w.u1 - w.u0, tb = w.base;
           const bool two = w.it.n - w.it.rb * tpb > p.tpt;
-          const int nq = two ? 2 * n : n;
+          // jobs of 64 keys: (tile, half, stream) with two row tiles, else (tile, half) and the tiles in turn
+          const int nq = two ? 4 * n : 2 * n;
+          const int last = two ? 3 : 1;              // the jobs of a tile, less one
           ok = mbar_wait(&qfull[0], items & 1, 0x523) && mbar_wait(&qfull[1], items & 1, 0x524);
           auto qk = [&](int q) {
-            const int s = q & 1, tile = tb + (two ? q >> 1 : q);
-            if (!two || s == 0) ok = ok && mbar_wait(&kfull[tile & 1], (tile >> 1) & 1, 0x525);
+            const int s = two ? q & 1 : (q >> 1) & 1, h = two ? (q >> 1) & 1 : q & 1, tile = tb + (two ? q >> 2 : q >> 1);
+            if ((q & last) == 0) ok = ok && mbar_wait(&kfull[tile & 1], (tile >> 1) & 1, 0x525);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
             t5_fence_after();
-            const uint64_t qa = dq + s * kStep, ka = dk + (tile & 1) * kStep;
+            const uint64_t qa = dq + s * kStep, ka = dk + (tile & 1) * kStep + ((h * 64 * 128) >> 4);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint64_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-              a5_mma_ss(lead, tmem + s * 128, qa + off, ka + off, id_s, k > 0 ? 1u : 0u);
+              a5_mma_ss(lead, tmem + s * 128 + h * 64, qa + off, ka + off, id_s, k > 0 ? 1u : 0u);
             }
-            a5_commit(lead, &sfull[s]);
-            if (!two || s == 1) a5_commit(lead, &kempty[tile & 1]);
+            a5_commit(lead, &sfull[2 * s + h]);
+            if ((q & last) == last) a5_commit(lead, &kempty[tile & 1]);
           };
           auto pv = [&](int q) {
-            const int s = q & 1, tile = tb + (two ? q >> 1 : q);
-            if (!two || s == 0) ok = ok && mbar_wait(&vfull[tile & 1], (tile >> 1) & 1, 0x526);
-            ok = ok && mbar_wait(&pfull[s], jobs[s] & 1, 0x527);
+            const int s = two ? q & 1 : (q >> 1) & 1, h = two ? (q >> 1) & 1 : q & 1, tile = tb + (two ? q >> 2 : q >> 1);
+            if ((q & last) == 0) ok = ok && mbar_wait(&vfull[tile & 1], (tile >> 1) & 1, 0x526);
+            ok = ok && mbar_wait(&pfull[2 * s + h], (turn >> s) & 1, 0x527);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
-            ++jobs[s];
+            if (h == 1) turn ^= 1u << s;
             t5_fence_after();
-            const uint64_t va = dv + (tile & 1) * kStep;
+            const uint64_t va = dv + (tile & 1) * kStep + ((h * 64 * 128) >> 4);
+            const bool fresh = h == 0 && q < 4;      // the stream's first job of the item
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              a5_mma_ts(lead, tmem + 256 + s * D, tmem + s * 128 + k * 8, va + ((k * 2048) >> 4), id_o, (q >= 2 || k > 0) ? 1u : 0u);
-            if (!two || s == 1) a5_commit(lead, &vempty[tile & 1]);
-            if (q + 2 >= nq) a5_commit(lead, &ofull[s]);
+            for (int k = 0; k < 4; ++k)
+              a5_mma_ts(lead, tmem + 256 + s * D, tmem + s * 128 + h * 64 + k * 8, va + ((k * 2048) >> 4), id_o,
+                        (!fresh || k > 0) ? 1u : 0u);
+            a5_commit(lead, &pvdone[2 * s + h]);
+            if ((q & last) == last) a5_commit(lead, &vempty[tile & 1]);
           };
-          if (ok) qk(0);
-          if (ok && nq > 1) qk(1);
-          if (ok && nq == 1) a5_commit(lead, &ofull[1]);   // the other stream has no tile
+          for (int q = 0; q < 4 && q < nq && ok; ++q) qk(q);
           for (int q = 0; q < nq && ok; ++q) {
             pv(q);
-            if (ok && q + 2 < nq) qk(q + 2);
+            if (ok && q + 4 < nq) qk(q + 4);
           }
           ++items;
           more = w.next(a, tpb);
@@ -419,7 +425,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
       const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t ts = tl + s * 128, to = tl + 256 + s * D;
       const int tok = tr / p.group, head = tr - tok * p.group;   // in the row tile
-      int items = 0, jobs = 0;
+      int jobs = 0;
       bool more = true, asked = false;               // asked: this item's q is on its way
       auto ask_q = [&](const Item& x) {
         if (tr == 0) {
@@ -446,16 +452,20 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         const int rlo = !valid ? 0 : a.window > 0 ? pos - a.window + 1 : 0;
         float m = -INFINITY, l = 0.f;
         const int nj = two ? n : (n - s + 1) / 2;
-        for (int q = 0; q < nj; ++q, ++jobs) {
-          const int tile = two ? q : 2 * q + s;
+        for (int q = 0; q < 2 * nj; ++q, ++jobs) {               // jobs: 64 keys of a tile
+          const int h = q & 1;
+          const int tile = two ? q >> 1 : 2 * (q >> 1) + s;
           const int jt = w.base + tile;
           const int slot = jt & (kA5ScaleSlots - 1);
-          if (ok) ok = mbar_wait(&scfull[slot], (jt / kA5ScaleSlots) & 1, 0x529);
-          if (ok) ok = mbar_wait(&sfull[s], jobs & 1, 0x52a);
+          if (ok && h == 0) ok = mbar_wait(&scfull[slot], (jt / kA5ScaleSlots) & 1, 0x529);
+          if (ok) ok = mbar_wait(&sfull[2 * s + h], (jobs >> 1) & 1, 0x52a);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           t5_fence_after();
-          if (two && q == nj - 1) {
+          float x[64];
+          a5_ld32(ts + h * 64, *reinterpret_cast<float(*)[32]>(&x[0]));
+          a5_ld32(ts + h * 64 + 32, *reinterpret_cast<float(*)[32]>(&x[32]));
+          if (two && q == 2 * nj - 1) {
             // the item's products with q are complete: the next item's rows may come in
             Walk<kA5T, kA5Ov> nx = w;
             if (nx.next(a, tpb)) {
@@ -463,115 +473,90 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
               asked = true;
             }
           }
-          const int k0 = (it.t0 + w.u0 + tile) * kA5T;
-          const uint32_t ssc = sb + S::oScales + slot * 128;
+          const int k0 = (it.t0 + w.u0 + tile) * kA5T + h * 64;
+          const uint32_t ssc = sb + S::oScales + slot * 128 + h * 64;
           const int clo = rlo - k0, chi = rhi - k0;              // columns that the row sees
-          // a warp whose rows all see the whole tile (nearly all of them) tests no key
-          const bool masked = __any_sync(0xffffffffu, clo > 0 || chi < kA5T);
-          // O and the first `chunks` chunks of P over to a higher bound
-          auto raise = [&](float to_m, int chunks) {
-            const float al = to_m == m ? 1.f : attn_ex2(m - to_m);   // 0 where there was nothing
-            m = to_m;
+          float4 sc[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) sc[g] = a5_lds_f4(ssc + g * 16);
+          a5_wait32(*reinterpret_cast<float(*)[32]>(&x[0]));
+          a5_wait32(*reinterpret_cast<float(*)[32]>(&x[32]));
+          // a warp whose rows all see all keys (nearly every one) tests none
+          if (__any_sync(0xffffffffu, clo > 0 || chi < 64)) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) x[i] = i >= clo && i < chi ? x[i] : -INFINITY;
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            float y = a5_max3(x[g * 16], x[g * 16 + 1], x[g * 16 + 2]);
+            float z = a5_max3(x[g * 16 + 3], x[g * 16 + 4], x[g * 16 + 5]);
+            y = a5_max3(y, x[g * 16 + 6], x[g * 16 + 7]);
+            z = a5_max3(z, x[g * 16 + 8], x[g * 16 + 9]);
+            y = a5_max3(y, x[g * 16 + 10], x[g * 16 + 11]);
+            z = a5_max3(z, x[g * 16 + 12], x[g * 16 + 13]);
+            y = a5_max3(y, x[g * 16 + 14], x[g * 16 + 15]);
+            y = fmaxf(y, z);
+            mx = fmaxf(mx, y == -INFINITY ? y : fmaf(y, sc[g].x, sc[g].y));
+          }
+          if (__any_sync(0xffffffffu, mx > m + kA5Slack)) {
+            // O goes over to the higher bound, once it has taken in every P before this one
+            const float nm = mx > m + kA5Slack ? mx : m;
+            const float al = nm == m ? 1.f : attn_ex2(m - nm);   // 0 where there was nothing
+            m = nm;
             l *= al;
-            a5_wait_st();
+            if (q > 0) {
+              ok = __all_sync(0xffffffffu, mbar_wait(&pvdone[2 * s + (h ^ 1)], ((jobs - 1) >> 1) & 1, 0x52c));
+              if (!ok) break;
+              t5_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < (q > 0 ? D : 0); c += 32) {
-              float v[32];
-              a5_get32(to + c, v);
-              uint32_t r0[16], r1[16];
+              for (int c = 0; c < D; c += 32) {
+                float v[32];
+                a5_get32(to + c, v);
+                uint32_t r0[16], r1[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                r0[i] = __float_as_uint(v[i] * al);
-                r1[i] = __float_as_uint(v[16 + i] * al);
-              }
-              a5_st16(to + c, r0);
-              a5_st16(to + c + 16, r1);
-            }
-#pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
-              float v[32];
-              a5_get32(ts + c * 16, v);                          // 16 columns of it are P
-              uint32_t r[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const uint32_t u = __float_as_uint(v[i]);
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
-                r[i] = a5_pack(f.x * al, f.y * al);
-              }
-              a5_st16(ts + c * 16, r);
-            }
-          };
-          // Chunks of 32 keys, three in flight: the weights of one, the maximum of the next, the load of
-          // the one after.
-          auto pass = [&](auto test) {
-            float v[3][32];
-            auto look = [&](int c) {                             // the chunk's maximum against the bound
-              float (&x)[32] = v[c % 3];
-              a5_wait32(x);
-              if (c < 3) a5_ld32(ts + (c + 1) * 32, v[(c + 1) % 3]);
-              float mx = -INFINITY;
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float4 sc = a5_lds_f4(ssc + (c * 2 + h) * 16);
-                if (decltype(test)::value) {
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) {
-                    const int col = c * 32 + h * 16 + i;
-                    x[h * 16 + i] = col >= clo && col < chi ? x[h * 16 + i] : -INFINITY;
-                  }
+                for (int i = 0; i < 16; ++i) {
+                  r0[i] = __float_as_uint(v[i] * al);
+                  r1[i] = __float_as_uint(v[16 + i] * al);
                 }
-                float y[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  y[i] = fmaxf(fmaxf(x[h * 16 + i], x[h * 16 + 4 + i]), fmaxf(x[h * 16 + 8 + i], x[h * 16 + 12 + i]));
-                const float z = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-                mx = fmaxf(mx, z == -INFINITY ? z : fmaf(z, sc.x, sc.y));
+                a5_st16(to + c, r0);
+                a5_st16(to + c + 16, r1);
               }
-              return mx;
-            };
-            auto settle = [&](float mx, int c, int written) {    // c: the chunk of mx; `written` chunks are P
-              if (__any_sync(0xffffffffu, mx > m + kA5Slack)) {
-                if (c < 3) a5_wait32(v[(c + 1) % 3]);
-                raise(mx > m + kA5Slack ? mx : m, written);
-              }
-            };
-            a5_ld32(ts, v[0]);
-            settle(look(0), 0, 0);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float nx = -INFINITY;
-              if (c < 3) nx = look(c + 1);
-              float (&x)[32] = v[c % 3];
-              const float base = m == -INFINITY ? 0.f : m;
-              uint32_t pk[16];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float4 sc = a5_lds_f4(ssc + (c * 2 + h) * 16);
-                const float2 kk = make_float2(sc.x, sc.x), bb = make_float2(sc.y - base, sc.y - base);
-                float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                  const float2 e = a5_fma2(make_float2(x[h * 16 + i], x[h * 16 + i + 1]), kk, bb);
-                  const float2 y = make_float2(attn_ex2(e.x), attn_ex2(e.y));
-                  sum = a5_add2(sum, y);
-                  pk[h * 8 + i / 2] = a5_pack(y.x, y.y);
-                }
-                l = fmaf(sum.x + sum.y, sc.z, l);
-              }
-              a5_st16(ts + c * 16, pk);                          // over columns of S that have been read
-              if (c < 3) settle(nx, c + 1, c + 1);
             }
-          };
-          if (masked) pass(A5Flag<true>{}); else pass(A5Flag<false>{});
+          }
+          const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const float4 f = sc[2 * c + g];
+              const float2 kk = make_float2(f.x, f.x), bb = make_float2(f.y - base, f.y - base);
+              float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                const int k = c * 32 + g * 16 + i;
+                const float2 e = a5_fma2(make_float2(x[k], x[k + 1]), kk, bb);
+                const float2 y = make_float2(attn_ex2(e.x), attn_ex2(e.y));
+                sum = a5_add2(sum, y);
+                pk[g * 8 + i / 2] = a5_pack(y.x, y.y);
+              }
+              l = fmaf(sum.x + sum.y, f.z, l);
+            }
+            a5_st16(ts + h * 64 + c * 16, pk);                   // over columns of S that have been read
+          }
           a5_wait_st();
           t5_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&pfull[s]);
+          if (lane == 0) mbar_arrive(&pfull[2 * s + h]);
         }
-        if (ok) ok = mbar_wait(&ofull[s], items & 1, 0x52b);
+        // the last two products of the item (the ones before are complete: their places hold the last S)
+        if (ok && nj > 0) {
+          const int ph = ((jobs - 1) >> 1) & 1;
+          ok = mbar_wait(&pvdone[2 * s], ph, 0x52b) && mbar_wait(&pvdone[2 * s + 1], ph, 0x52d);
+        }
         ok = __all_sync(0xffffffffu, ok);
         t5_fence_after();
-        ++items;
         // ---------------------------------------------------------------- the item's result
         const bool whole = w.whole();
         const int c0 = w.first_cta(sp), c1 = w.last_cta(sp);
