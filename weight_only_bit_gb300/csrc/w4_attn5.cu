@@ -44,8 +44,8 @@ constexpr int kA5R = 256;                    // rows per item, at most
 constexpr int kA5Ov = 2;                     // what an item costs beside its tiles
 constexpr int kA5Mma = 12;                   // the issuing warp
 constexpr int kA5Threads = 512;
-// Registers a thread: launched with 128 each (65536 in all); 2 x 128 x 168 + 128 x 128 + 128 x 48 = 65536.
-constexpr int kA5RegsSoftmax = 168, kA5RegsMma = 48;
+// Registers a thread: launched with 128 each (65536 in all); 2 x 128 x 152 + 128 x 128 + 128 x 80 = 65536.
+constexpr int kA5RegsSoftmax = 152, kA5RegsMma = 80;
 constexpr float kA5Slack = 6.f;
 constexpr int kA5ScaleSlots = 4;
 
