@@ -2,7 +2,9 @@
 //
 // Mathematics.  p = softmax(x / T) is needed at the drafted tokens of every position and over the whole
 // vocabulary at one position per sequence (the first refused one, or the last).  So: one pass over
-// all logits for each row's maximum m and sum of 2^((x - m) c), c = log2(e) / T; then the decisions
+// all logits for each row's reference m (the largest x c, rounded) and sum of 2^(x c - m), c = log2(e) / T,
+// one fused multiply-add and one exponential per logit: m's rounding is in the sum and in every
+// probability alike and cancels; then the decisions
 // from a few gathered values; then one row per sequence again for the race
 // argmax_v max(p - q, 0)(v) / e(v), which draws from the residual distribution without a sum over it
 // (the smallest of independent exponential times e / w is at v with probability w_v / sum w).
@@ -13,7 +15,8 @@
 // the second, every CTA of a sequence joins the pieces in index order (the same bits in each CTA),
 // decides, and runs its part of the race; the last CTA to finish (a ticket per sequence) takes the best
 // part and writes the answer.  Best is the largest (score, lowest token) as one 64-bit key, so the
-// order of arrival does not matter.
+// order of arrival does not matter.  Scores are compared by an approximate quotient first; only what
+// comes within its error of the best so far is divided exactly.
 // What bounds it: DRAM bytes of the logits for a batch, launches and dependent loads for one sequence.
 #include <cstdint>
 #include <cuda_fp16.h>
@@ -30,39 +33,40 @@ constexpr int kVfMaxPieces = 64;            // pieces of one row in the first la
 constexpr int kVfMaxParts = 64;             // CTAs of one sequence in the second
 
 struct VerifyPlan {
-  int pieces, piece;                        // per row; tokens of a piece (a multiple of 8)
+  int pieces, piece;                        // per row; 8-token vectors of a piece
   int parts, part;                          // per sequence; tokens of a part (a multiple of 8)
 };
 
 static VerifyPlan plan_verify(int batch, int rows, int vocab, int sms) {
   VerifyPlan p;
-  // about four CTAs per SM in flight, at least 4096 tokens each (16 a thread)
-  const long long want = 4LL * sms;
+  // about eight CTAs per SM, at least 4096 tokens each (16 a thread)
+  const long long want = 8LL * sms;
   auto cut = [&](long long n, int most) {
-    long long k = (want + n - 1) / n;
+    long long k = want / n;
     const long long fit = (vocab + 4095) / 4096;
     if (k > fit) k = fit;
     if (k > most) k = most;
     return (int)(k < 1 ? 1 : k);
   };
+  const int vecs = vocab / 8 + 1;
   p.pieces = cut((long long)batch * rows, kVfMaxPieces);
-  p.piece = ((vocab + p.pieces - 1) / p.pieces + 7) & ~7;
-  p.pieces = (vocab + p.piece - 1) / p.piece;
-  p.parts = cut(batch, kVfMaxParts);
+  p.piece = (vecs + p.pieces - 1) / p.pieces;
+  p.pieces = (vecs + p.piece - 1) / p.piece;
+  p.parts = cut(2LL * batch, kVfMaxParts);
   p.part = ((vocab + p.parts - 1) / p.parts + 7) & ~7;
   p.parts = (vocab + p.part - 1) / p.part;
   return p;
 }
 
-// Workspace: [batch] tickets, [batch][kVfMaxParts][2] keys, [rows][kVfMaxPieces] (maximum, sum, first
-// token with the maximum, unused).
+// Workspace: [batch] tickets, [batch][kVfMaxParts] keys, [rows][kVfMaxPieces] (reference, sum,
+// first token with the largest logit, that logit; the last two at temperature 0).
 struct VerifyWs {
   unsigned int* ticket;
   unsigned long long* keys;
   float4* stats;
 };
 __host__ __device__ inline size_t vf_keys_at(int batch) { return ((size_t)batch * 4 + 15) & ~(size_t)15; }
-__host__ __device__ inline size_t vf_stats_at(int batch) { return vf_keys_at(batch) + (size_t)batch * kVfMaxParts * 16; }
+__host__ __device__ inline size_t vf_stats_at(int batch) { return vf_keys_at(batch) + (size_t)batch * kVfMaxParts * 8; }
 
 int64_t verify_workspace_bytes(int batch, int drafts, int vocab) {
   (void)vocab;
@@ -87,23 +91,42 @@ __device__ __forceinline__ float vf_logit(__half h) {
   return x != x ? -INFINITY : fminf(x, 65504.f);
 }
 
-// Eight logits of a row from token v on (v a multiple of 8), whatever the row's alignment; -infinity
-// past the end.
-__device__ __forceinline__ void vf_load8(const __half* row, int v, int end, float (&x)[8]) {
-  if (v + 8 <= end && ((reinterpret_cast<uintptr_t>(row + v) & 15) == 0)) {
-    const uint4 w = ld_nc_v4(row + v);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 p = *reinterpret_cast<const __half2*>(&u[i]);
-      x[2 * i] = vf_logit(__low2half(p));
-      x[2 * i + 1] = vf_logit(__high2half(p));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = v + i < end ? vf_logit(row[v + i]) : -INFINITY;
-  }
+// The same for two at once.
+__device__ __forceinline__ uint32_t vf_logit2(uint32_t u) {
+  const __half2 x = __hmin2(__hmax2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0xfc00))),
+                            __half2half2(__ushort_as_half(0x7bff)));
+  return *reinterpret_cast<const uint32_t*>(&x);
 }
+
+// Eight logits of a row from token v on, whatever the alignment, as they lie in memory; -infinity past
+// the end.
+__device__ __forceinline__ uint4 vf_load8(const __half* row, int v, int end) {
+  const __half* p = row + v;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  if (v + 8 <= end) {
+    if ((at & 15) == 0) return ld_nc_v4(p);
+    uint32_t u[4];
+    if ((at & 3) == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+    } else {
+      const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = (uint32_t)__ldg(q + 2 * i) | (uint32_t)__ldg(q + 2 * i + 1) << 16;
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  uint32_t u[4];
+  const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = v + 2 * i < end ? __ldg(q + 2 * i) : 0xfc00u, hi = v + 2 * i + 1 < end ? __ldg(q + 2 * i + 1) : 0xfc00u;
+    u[i] = lo | hi << 16;
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+__device__ __forceinline__ float2 vf_pair(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
 
 // Key of (value, token): larger value first, then the lower token.  Values are not NaN.
 __device__ __forceinline__ unsigned long long vf_key(float x, int v) {
@@ -125,11 +148,11 @@ __device__ __forceinline__ unsigned long long vf_warp_max(unsigned long long k) 
   return k;
 }
 
-// Joins two (maximum, sum) pairs.
-__device__ __forceinline__ float2 vf_join(float2 a, float2 b, float c) {
+// Joins two (reference, sum) pairs.
+__device__ __forceinline__ float2 vf_join(float2 a, float2 b) {
   const float m = fmaxf(a.x, b.x);
   if (m == -INFINITY) return make_float2(m, 0.f);
-  return make_float2(m, a.y * vf_ex2((a.x - m) * c) + b.y * vf_ex2((b.x - m) * c));
+  return make_float2(m, a.y * vf_ex2(a.x - m) + b.y * vf_ex2(b.x - m));
 }
 
 // Row r of a sequence: target rows 0 ... drafts, then the draft's rows.
@@ -143,6 +166,7 @@ __device__ __forceinline__ int vf_count(const VerifyArgs& a, int b) {
 }
 
 // First launch: CTA = one piece of one row.
+template <bool GREEDY>
 __global__ void __launch_bounds__(kVfThreads) w4_verify_stats_kernel(const __grid_constant__ VerifyArgs a, VerifyPlan pl,
                                                                      int rows) {
   __shared__ float2 red[kVfThreads / 32];
@@ -156,46 +180,97 @@ __global__ void __launch_bounds__(kVfThreads) w4_verify_stats_kernel(const __gri
   const int n = vf_count(a, b);
   if (r <= a.drafts ? r > n : r - a.drafts - 1 >= n) return;      // a row that nothing reads
   const __half* row = vf_row(a, b, r);
-  const int v0 = piece * pl.piece, v1 = min(v0 + pl.piece, a.vocab);
-  const bool greedy = a.temperature == 0.f;
-  const float c = 1.4426950408889634f / (greedy ? 1.f : a.temperature);
-  float2 s = make_float2(-INFINITY, 0.f);
-  unsigned long long key = 0;
-  for (int v = v0 + tid * 8; v < v1; v += kVfThreads * 16) {
-    float x[16];
-    vf_load8(row, v, v1, *reinterpret_cast<float(*)[8]>(&x[0]));
-    const int w = v + kVfThreads * 8;
-    if (w < v1) vf_load8(row, w, v1, *reinterpret_cast<float(*)[8]>(&x[8]));
-    else {
+  // 16-byte vectors from the row's first aligned token on; the few tokens before and after go with piece 0
+  const int head = min((int)(((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) >> 1), a.vocab);
+  const int vecs = (a.vocab - head) / 8;
+  const int k1 = min((piece + 1) * pl.piece, vecs);
+  const __half* base = row + head;
+  const float c = 1.4426950408889634f / (GREEDY ? 1.f : a.temperature);
+  float top = -INFINITY, m = -INFINITY, sum = 0.f;   // largest logit, m = top c, sum of 2^(x c - m)
+  int at = -1;                               // GREEDY: the first token with the largest logit
+  // joins 32 logits; `clean`: NaN and +infinity replaced
+  auto take = [&](uint32_t (&u)[16], int k) {
+    __half2 h = *reinterpret_cast<const __half2*>(&u[0]);
 #pragma unroll
-      for (int i = 8; i < 16; ++i) x[i] = -INFINITY;
+    for (int i = 1; i < 16; ++i) h = __hmax2(h, *reinterpret_cast<const __half2*>(&u[i]));   // passes over NaNs
+    float mx = fmaxf(__low2float(h), __high2float(h));
+    auto add = [&] {
+      if (mx > top) {
+        if (GREEDY) {
+#pragma unroll
+          for (int i = 15; i >= 0; --i) {
+            const float2 f = vf_pair(u[i]);
+            const int t = head + 8 * (k + (i >> 2) * kVfThreads) + (i & 3) * 2;
+            if (f.y == mx) at = t + 1;
+            if (f.x == mx) at = t;
+          }
+        }
+        top = mx;
+        sum *= vf_ex2(m - mx * c);           // 0 where there was nothing
+        m = mx * c;
+      }
+      const float z = m == -INFINITY ? 0.f : m;
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 f = vf_pair(u[i]);
+        s[(2 * i) & 3] += vf_ex2(fmaf(f.x, c, -z));
+        s[(2 * i + 1) & 3] += vf_ex2(fmaf(f.y, c, -z));
+      }
+      return (s[0] + s[1]) + (s[2] + s[3]);
+    };
+    const float t0 = top, m0 = m, s0 = sum;
+    const int at0 = at;
+    float s = mx < INFINITY ? add() : NAN;
+    if (s != s) {
+      // a NaN or an infinity among them: again, with what they stand for
+      top = t0;
+      m = m0;
+      sum = s0;
+      at = at0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) u[i] = vf_logit2(u[i]);
+      mx = fminf(mx, 65504.f);
+      s = add();
     }
-    float m = x[0];
+    sum += s;
+  };
+  for (int k = piece * pl.piece + tid; k < k1; k += kVfThreads * 4) {
+    uint4 w[4];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) m = fmaxf(m, x[i]);
-    if (greedy && m > s.x) {
-      // the first token with this value, in index order (v before w)
-      int at = 0;
-#pragma unroll
-      for (int i = 15; i >= 0; --i)
-        if (x[i] == m) at = i;
-      key = vf_max(key, vf_key(m, at < 8 ? v + at : w + at - 8));
+    for (int i = 0; i < 4; ++i) {
+      w[i] = make_uint4(0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u);
+      if (k + i * kVfThreads < k1) w[i] = ld_nc_v4(base + 8 * (size_t)(k + i * kVfThreads));
     }
-    const float nm = fmaxf(s.x, m);
-    if (nm != -INFINITY) {
-      float sum = 0.f;
+    uint32_t u[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sum += vf_ex2((x[i] - nm) * c);
-      s.y = s.y * vf_ex2((s.x - nm) * c) + sum;
-      s.x = nm;
+    for (int i = 0; i < 4; ++i) {
+      u[4 * i] = w[i].x;
+      u[4 * i + 1] = w[i].y;
+      u[4 * i + 2] = w[i].z;
+      u[4 * i + 3] = w[i].w;
+    }
+    take(u, k);
+  }
+  unsigned long long key = GREEDY ? vf_key(top, at) : 0;
+  if (piece == 0) {
+    // up to 7 tokens before the vectors and up to 7 after them
+    const int t = tid < head ? tid : tid >= 32 && tid < 40 ? head + 8 * vecs + tid - 32 : a.vocab;
+    if (t < a.vocab) {
+      const float x = vf_logit(row[t]);
+      const float2 s = vf_join(make_float2(m, sum), make_float2(x * c, x == -INFINITY ? 0.f : 1.f));
+      m = s.x;
+      sum = s.y;
+      if (GREEDY) key = vf_max(key, vf_key(x, t));
     }
   }
+  float2 s = make_float2(m, sum);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float2 t = make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o));
-    s = vf_join(s, t, c);
+    s = vf_join(s, t);
   }
-  if (greedy) key = vf_warp_max(key);
+  if (GREEDY) key = vf_warp_max(key);
   if (lane == 0) {
     red[warp] = s;
     redk[warp] = key;
@@ -204,48 +279,50 @@ __global__ void __launch_bounds__(kVfThreads) w4_verify_stats_kernel(const __gri
   if (tid == 0) {
 #pragma unroll
     for (int w = 1; w < kVfThreads / 32; ++w) {
-      s = vf_join(s, red[w], c);
+      s = vf_join(s, red[w]);
       key = vf_max(key, redk[w]);
     }
     const VerifyWs ws = vf_ws(a.workspace, a.batch);
-    ws.stats[(size_t)br * kVfMaxPieces + piece] = make_float4(s.x, s.y, __int_as_float(vf_key_token(key)), 0.f);
+    ws.stats[(size_t)br * kVfMaxPieces + piece] = make_float4(s.x, s.y, __int_as_float(vf_key_token(key)), vf_key_value(key));
   }
 }
 
-// Whole-row statistics from the pieces, by a warp (every lane gets the result): the maximum, log2 of the
-// sum of 2^((x - m) c), and the first token with the maximum.
+// Whole-row statistics from the pieces, by a warp (every lane gets the result): the reference, log2 of the
+// sum of 2^(x c - m), and the first token with the largest logit.
 struct RowStat {
   float m, lg;
   int at;
 };
-__device__ __forceinline__ RowStat vf_row_stat(const VerifyWs& ws, int br, int pieces, float c, int lane) {
+__device__ __forceinline__ RowStat vf_row_stat(const VerifyWs& ws, int br, int pieces, bool greedy, int lane) {
   float2 s = make_float2(-INFINITY, 0.f);
   unsigned long long key = 0;
   for (int i = lane; i < pieces; i += 32) {
     const float4 f = __ldcg(ws.stats + (size_t)br * kVfMaxPieces + i);
-    s = vf_join(s, make_float2(f.x, f.y), c);
-    key = vf_max(key, vf_key(f.x, __float_as_int(f.z)));
+    s = vf_join(s, make_float2(f.x, f.y));
+    if (greedy) key = vf_max(key, vf_key(f.w, __float_as_int(f.z)));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     // both partners add in the same order, so that every lane holds the same bits
     const float2 t = make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o));
-    s = (lane & o) ? vf_join(t, s, c) : vf_join(s, t, c);
+    s = (lane & o) ? vf_join(t, s) : vf_join(s, t);
   }
-  key = vf_warp_max(key);
+  if (greedy) key = vf_warp_max(key);
   return {s.x, s.y > 0.f ? log2f(s.y) : -INFINITY, vf_key_token(key)};
 }
 
-// Probability of a logit in a row with these statistics; 0 for a row without any finite logit.
+// log2 of a logit's probability in a row with these statistics.
+__device__ __forceinline__ float vf_log2p(float x, const RowStat& s, float c) { return fmaf(x, c, -s.m) - s.lg; }
+// The probability; 0 for a row without any finite logit.
 __device__ __forceinline__ float vf_prob(float x, const RowStat& s, float c) {
-  return x == -INFINITY || s.m == -INFINITY ? 0.f : vf_ex2((x - s.m) * c - s.lg);
+  return x == -INFINITY ? 0.f : vf_ex2(vf_log2p(x, s, c));
 }
 
 // Second launch: CTA = one part of one sequence's race.
 __global__ void __launch_bounds__(kVfThreads) w4_verify_pick_kernel(const __grid_constant__ VerifyArgs a, VerifyPlan pl,
                                                                     int rows) {
   __shared__ RowStat stat[2 * W4_MAX_DRAFTS + 1];
-  __shared__ unsigned long long red[kVfThreads / 32][2];
+  __shared__ unsigned long long red[kVfThreads / 32];
   __shared__ int s_last;
   pdl_launch_dependents();
   pdl_wait();
@@ -259,7 +336,7 @@ __global__ void __launch_bounds__(kVfThreads) w4_verify_pick_kernel(const __grid
   const bool with_q = rows > a.drafts + 1;
   for (int r = warp; r < rows; r += kVfThreads / 32) {
     if (r <= a.drafts ? r > n : r - a.drafts - 1 >= n) continue;
-    const RowStat s = vf_row_stat(ws, b * rows + r, pl.pieces, c, lane);
+    const RowStat s = vf_row_stat(ws, b * rows + r, pl.pieces, greedy, lane);
     if (lane == 0) stat[r] = s;
   }
   __syncthreads();
@@ -272,7 +349,7 @@ __global__ void __launch_bounds__(kVfThreads) w4_verify_pick_kernel(const __grid
     if (x >= 0 && x < a.vocab) {
       const RowStat s = stat[lane];
       const float logit = vf_logit(vf_row(a, b, lane)[x]);
-      lp = ((logit - s.m) * c - s.lg) * 0.6931471805599453f;
+      lp = logit == -INFINITY ? -INFINITY : vf_log2p(logit, s, c) * 0.6931471805599453f;
       if (greedy) {
         refuse = !(s.at == x && s.m != -INFINITY);
       } else {
@@ -284,7 +361,7 @@ __global__ void __launch_bounds__(kVfThreads) w4_verify_pick_kernel(const __grid
     }
   }
   const int acc = __ffs(__ballot_sync(0xffffffffu, refuse)) - 1;   // lane n always refuses
-  unsigned long long best = 0, plain = 0;    // of the residual, and of p alone
+  unsigned long long best = 0;
   if (!greedy) {
     const __half* row = vf_row(a, b, acc);
     const RowStat s = stat[acc];
@@ -294,69 +371,88 @@ __global__ void __launch_bounds__(kVfThreads) w4_verify_pick_kernel(const __grid
     const RowStat sq = q_row ? stat[a.drafts + 1 + acc] : s;
     const int certain = residual && !with_q ? __shfl_sync(0xffffffffu, x, acc) : -1;
     const float* e = a.e + (long long)b * a.vocab;
-    const int v0 = part * pl.part, v1 = min(v0 + pl.part, a.vocab);
-    for (int v = v0 + tid * 8; v < v1; v += kVfThreads * 8) {
-      float px[8], qx[8], ee[8];
-      vf_load8(row, v, v1, px);
-      if (q_row) vf_load8(qrow, v, v1, qx);
-      if (v + 8 <= v1 && ((reinterpret_cast<uintptr_t>(e + v) & 15) == 0)) {
+    // argmax of w / e over [v0, v1), w = p - q, p without the certain token, or (plain) p; whole warps.
+    // Approximate quotients (within 2^-21) set a bound for the warp; what reaches it is divided exactly.
+    auto race = [&](int v0, int v1, bool plain) {
+      const bool minus = q_row && !plain;
+      float top = 0.f, near = 0.f;
+      int at = -1;
+      for (int vw = v0 + warp * 256; vw < v1; vw += kVfThreads * 8) {
+        const int v = vw + lane * 8;
+        float f[8], w[8], ee[8], hi = 0.f;
+        if (v < v1) {
+          const uint4 pw = vf_load8(row, v, v1);
+          const uint4 qw = minus ? vf_load8(qrow, v, v1) : pw;
+          if (v + 8 <= v1 && ((reinterpret_cast<uintptr_t>(e + v) & 15) == 0)) {
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const float4 f = __ldg(reinterpret_cast<const float4*>(e + v + i));
-          ee[i] = f.x; ee[i + 1] = f.y; ee[i + 2] = f.z; ee[i + 3] = f.w;
+            for (int i = 0; i < 8; i += 4) {
+              const float4 y = __ldg(reinterpret_cast<const float4*>(e + v + i));
+              ee[i] = y.x; ee[i + 1] = y.y; ee[i + 2] = y.z; ee[i + 3] = y.w;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ee[i] = v + i < v1 ? __ldg(e + v + i) : 1.f;
+          }
+          const uint32_t pu[4] = {pw.x, pw.y, pw.z, pw.w}, qu[4] = {qw.x, qw.y, qw.z, qw.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 px = vf_pair(vf_logit2(pu[i])), qx = vf_pair(vf_logit2(qu[i]));
+            w[2 * i] = vf_prob(px.x, s, c);
+            w[2 * i + 1] = vf_prob(px.y, s, c);
+            if (minus) {
+              w[2 * i] -= vf_prob(qx.x, sq, c);
+              w[2 * i + 1] -= vf_prob(qx.y, sq, c);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (!plain && v + i == certain) w[i] = 0.f;
+            f[i] = w[i] > 0.f ? __fdividef(w[i], ee[i]) : 0.f;
+            hi = fmaxf(hi, f[i]);
+          }
         }
-      } else {
+        near = fmaxf(near, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(hi))) * (1.f - 1e-6f));
+        if (hi >= near && v < v1) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ee[i] = v + i < v1 ? __ldg(e + v + i) : 1.f;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float p = vf_prob(px[i], s, c);
-        if (p > 0.f) {
-          const float d = __fdiv_rn(p, ee[i]);
-          if (d >= 0.f) plain = vf_max(plain, vf_key(d, v + i));
-          float w = p;
-          if (q_row) w = p - vf_prob(qx[i], sq, c);
-          else if (v + i == certain) w = 0.f;
-          if (w > 0.f) {
-            const float f = __fdiv_rn(w, ee[i]);
-            if (f >= 0.f) best = vf_max(best, vf_key(f, v + i));
+          for (int i = 0; i < 8; ++i) {
+            if (w[i] > 0.f && f[i] >= near) {
+              const float x = __fdiv_rn(w[i], ee[i]);
+              if (x > top) {
+                top = x;
+                at = v + i;
+              }
+            }
           }
         }
       }
-    }
-    best = vf_warp_max(best);
-    plain = vf_warp_max(plain);
-    if (lane == 0) {
-      red[warp][0] = best;
-      red[warp][1] = plain;
-    }
+      return at >= 0 ? vf_key(top, at) : 0ull;
+    };
+    const int v0 = part * pl.part;
+    best = vf_warp_max(race(v0, min(v0 + pl.part, a.vocab), false));
+    if (lane == 0) red[warp] = best;
     __syncthreads();
     if (tid == 0) {
 #pragma unroll
-      for (int w = 1; w < kVfThreads / 32; ++w) {
-        best = vf_max(best, red[w][0]);
-        plain = vf_max(plain, red[w][1]);
-      }
-      unsigned long long* k = ws.keys + ((size_t)b * kVfMaxParts + part) * 2;
-      k[0] = best;
-      k[1] = plain;
+      for (int w = 1; w < kVfThreads / 32; ++w) best = vf_max(best, red[w]);
+      ws.keys[(size_t)b * kVfMaxParts + part] = best;
       __threadfence();
       s_last = atomicAdd(ws.ticket + b, 1u) == (unsigned)pl.parts - 1u;
     }
     __syncthreads();
     if (!s_last) return;
-    if (warp != 0) return;
     __threadfence();
-    best = plain = 0;
-    for (int i = lane; i < pl.parts; i += 32) {
-      const unsigned long long* k = ws.keys + ((size_t)b * kVfMaxParts + i) * 2;
-      best = vf_max(best, __ldcg(k));
-      plain = vf_max(plain, __ldcg(k + 1));
-    }
+    best = 0;
+    for (int i = lane; i < pl.parts; i += 32) best = vf_max(best, __ldcg(ws.keys + (size_t)b * kVfMaxParts + i));
     best = vf_warp_max(best);
-    plain = vf_warp_max(plain);
-    if (best == 0) best = plain;
+    if (best == 0) {
+      // no token is likelier than in the draft (the two distributions are the same to rounding), or none
+      // has a probability: the race over p alone, by this CTA
+      best = vf_warp_max(race(0, a.vocab, true));
+      if (lane == 0) red[warp] = best;
+      __syncthreads();
+      for (int w = 0; w < kVfThreads / 32; ++w) best = vf_max(best, red[w]);
+    }
+    if (warp != 0) return;
     if (lane == 0) ws.ticket[b] = 0;         // ready for the next call
   } else if (part != 0 || warp != 0) {
     return;
@@ -370,7 +466,7 @@ __global__ void __launch_bounds__(kVfThreads) w4_verify_pick_kernel(const __grid
   } else if (best != 0) {
     token = vf_key_token(best);
   }
-  if (token >= 0) tlp = ((vf_logit(vf_row(a, b, acc)[token]) - s.m) * c - s.lg) * 0.6931471805599453f;
+  if (token >= 0) tlp = vf_log2p(vf_logit(vf_row(a, b, acc)[token]), s, c) * 0.6931471805599453f;
   if (lane <= a.drafts) {
     const long long o = (long long)b * (a.drafts + 1) + lane;
     a.tokens[o] = lane < acc ? x : lane == acc ? token : -1;
@@ -397,7 +493,8 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3((unsigned)g1);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, w4_verify_stats_kernel, a, pl, rows);
+  cudaError_t e = a.temperature > 0.f ? cudaLaunchKernelEx(&cfg, w4_verify_stats_kernel<false>, a, pl, rows)
+                                      : cudaLaunchKernelEx(&cfg, w4_verify_stats_kernel<true>, a, pl, rows);
   if (e != cudaSuccess) return e;
   note_launch();
   cfg.gridDim = dim3((unsigned)g2);
