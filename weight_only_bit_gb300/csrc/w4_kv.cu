@@ -9,9 +9,11 @@
 // range (2^-6 s) lose bits.  A power of two costs up to one binade of that range and no precision.
 //
 // Work split.  One CTA per (sequence, touched page, kv head) does K and V of the new rows in the page:
-// it needs both, because a NaN in a token's v marks the token's key.  It reads the rows twice, once
-// for amax and once to write the codes (the second read comes from L1): a page of 64 rows is 16 KB of
-// each, too much for registers at a useful occupancy.  Rows of q need no such unit: a warp per row.
+// it needs both, because a NaN in a token's v marks the token's key.  The rows are wanted twice, for
+// amax and for the codes, and are read twice, the second time from L1 or L2: kept in registers (64 rows of
+// 128 channels are 64 of them a thread) they cost more in occupancy than they saved (two prompts of
+// 8191 tokens, 32 + 2 x 8 heads: 86 us with all held at 152 registers, 72 with half at 96, 70 with
+// none at 80).  Rows of q need no such unit: a warp per row, four heads' loads in flight per lane.
 // What bounds it: DRAM bytes for prompts (q read and written, k and v read, codes written), launch
 // latency for single tokens.
 #include <cstdint>
@@ -32,8 +34,7 @@ struct Rot {
   float c[8], s[8];
 };
 
-__device__ __forceinline__ void load8(const __half* p, float (&x)[8]) {
-  const uint4 w = ld_nc_v4(p);
+__device__ __forceinline__ void widen8(uint4 w, float (&x)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -110,10 +111,18 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
+// Eight values over a scale.  The scale is a power of two unless an older one of another kind is larger:
+// then its reciprocal is exact and a product replaces the division.
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float s) {
   float y[8];
+  if ((__float_as_uint(s) & 0x7fffffu) == 0) {
+    const float f = __uint_as_float((254u << 23) - __float_as_uint(s));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], s);
+    for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(x[i], f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], s);
+  }
   return make_uint2(e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16, e4m3x2(y[4], y[5]) | e4m3x2(y[6], y[7]) << 16);
 }
 
@@ -142,7 +151,7 @@ __device__ __forceinline__ int find_seq(const int32_t* q_start, int batch, int t
 }
 
 template <int D>
-__global__ void __launch_bounds__(kKvThreads) w4_kv_append_kernel(const __grid_constant__ AppendArgs a, int upb) {
+__global__ void __launch_bounds__(kKvThreads, 6) w4_kv_append_kernel(const __grid_constant__ AppendArgs a, int upb) {
   constexpr int LPR = D / 16;                 // lanes per row
   constexpr int RPP = kKvThreads / LPR;       // rows per pass
   __shared__ float red[kKvThreads / 32][2];
@@ -170,22 +179,35 @@ __global__ void __launch_bounds__(kKvThreads) w4_kv_append_kernel(const __grid_c
     Rot r;
     const bool rot = ck.rot && ok;
     if (rot) load_rot(a, pos, l, r);
-    for (int h = lane / LPR; h < a.q_heads; h += 32 / LPR) {
-      const __half* src = a.q + (long long)t * a.q_stride + (long long)h * D;
-      __half* dst = a.q_out + (long long)t * a.q_out_stride + (long long)h * D;
-      float x0[8], x1[8];
-      load8(src + 8 * ck.c0, x0);
-      load8(src + 8 * ck.c1, x1);
-      if (rot) rotate(x0, x1, r, a.interleaved);
-      uint32_t w[8];
+    constexpr int HPP = 32 / LPR;            // heads per pass
+    const __half* src = a.q + (long long)t * a.q_stride + (long long)(lane / LPR) * D;
+    __half* dst = a.q_out + (long long)t * a.q_out_stride + (long long)(lane / LPR) * D;
+    for (int h = lane / LPR; h < a.q_heads; h += 4 * HPP, src += 4 * HPP * D, dst += 4 * HPP * D) {
+      uint4 r0[4], r1[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2 u = __floats2half2_rn(x0[2 * i], x0[2 * i + 1]), v = __floats2half2_rn(x1[2 * i], x1[2 * i + 1]);
-        w[i] = ok ? *reinterpret_cast<const uint32_t*>(&u) : 0u;
-        w[4 + i] = ok ? *reinterpret_cast<const uint32_t*>(&v) : 0u;
+      for (int k = 0; k < 4; ++k) {
+        if (h + k * HPP < a.q_heads) {
+          r0[k] = ld_nc_v4(src + k * HPP * D + 8 * ck.c0);
+          r1[k] = ld_nc_v4(src + k * HPP * D + 8 * ck.c1);
+        }
       }
-      *reinterpret_cast<uint4*>(dst + 8 * ck.c0) = make_uint4(w[0], w[1], w[2], w[3]);
-      *reinterpret_cast<uint4*>(dst + 8 * ck.c1) = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (h + k * HPP >= a.q_heads) break;
+        float x0[8], x1[8];
+        widen8(r0[k], x0);
+        widen8(r1[k], x1);
+        if (rot) rotate(x0, x1, r, a.interleaved);
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2 u = __floats2half2_rn(x0[2 * i], x0[2 * i + 1]), v = __floats2half2_rn(x1[2 * i], x1[2 * i + 1]);
+          w[i] = ok ? *reinterpret_cast<const uint32_t*>(&u) : 0u;
+          w[4 + i] = ok ? *reinterpret_cast<const uint32_t*>(&v) : 0u;
+        }
+        *reinterpret_cast<uint4*>(dst + k * HPP * D + 8 * ck.c0) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(dst + k * HPP * D + 8 * ck.c1) = make_uint4(w[4], w[5], w[6], w[7]);
+      }
     }
     return;
   }
@@ -213,17 +235,24 @@ __global__ void __launch_bounds__(kKvThreads) w4_kv_append_kernel(const __grid_c
   const int t0 = start + pg * P - (total - n);      // row of q, k, v of the page's row 0
   uint8_t* kb = a.c.k + (long long)id * a.c.page_stride + (long long)h * P * D;
   uint8_t* vb = a.c.v + (long long)id * a.c.page_stride + (long long)h * P * D;
-  // one row's 16 k and 16 v values of this lane, k rotated; nan: a NaN among the row's values
-  auto fetch = [&](int row, float (&k0)[8], float (&k1)[8], float (&v0)[8], float (&v1)[8]) -> bool {
-    const int t = t0 + row;
-    const __half* ks = a.k + (long long)t * a.k_stride + (long long)h * D;
-    const __half* vs = a.v + (long long)t * a.v_stride + (long long)h * D;
-    load8(ks + 8 * ck.c0, k0);
-    load8(ks + 8 * ck.c1, k1);
-    load8(vs + 16 * l, v0);
-    load8(vs + 16 * l + 8, v1);
+  // one row's 16 k and 16 v values of this lane, as they are in memory
+  struct Raw {
+    uint4 k0, k1, v0, v1;
+  };
+  auto fetch = [&](int row) {
+    const long long t = t0 + row;
+    const __half* ks = a.k + t * a.k_stride + (long long)h * D;
+    const __half* vs = a.v + t * a.v_stride + (long long)h * D;
+    return Raw{ld_nc_v4(ks + 8 * ck.c0), ld_nc_v4(ks + 8 * ck.c1), ld_nc_v4(vs + 16 * l), ld_nc_v4(vs + 16 * l + 8)};
+  };
+  // in FP32, k rotated; false: the row's rotary position is out of range
+  auto open = [&](const Raw& x, int row, float (&k0)[8], float (&k1)[8], float (&v0)[8], float (&v1)[8]) -> bool {
+    widen8(x.k0, k0);
+    widen8(x.k1, k1);
+    widen8(x.v0, v0);
+    widen8(x.v1, v1);
     if (a.rotary_dim > 0) {
-      const int pos = a.positions ? __ldg(a.positions + t) : pg * P + row;
+      const int pos = a.positions ? __ldg(a.positions + t0 + row) : pg * P + row;
       if (pos < 0 || pos >= a.max_position) return false;
       if (ck.rot) {
         Rot r;
@@ -235,18 +264,20 @@ __global__ void __launch_bounds__(kKvThreads) w4_kv_append_kernel(const __grid_c
   };
   auto finite_abs = [](float x) { return fabsf(x) <= 3.402823466e38f ? fabsf(x) : 0.f; };
   float ak = 0.f, av = 0.f;
-  for (int row = r0 + tid / LPR; row < r1; row += RPP) {
+  auto measure = [&](const Raw& x, int row) {
     float k0[8], k1[8], v0[8], v1[8];
-    if (!fetch(row, k0, k1, v0, v1)) {
+    if (!open(x, row, k0, k1, v0, v1)) {
       kv_range_error(0x403);
-      continue;
+      return;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       ak = fmaxf(ak, fmaxf(finite_abs(k0[i]), finite_abs(k1[i])));
       av = fmaxf(av, fmaxf(finite_abs(v0[i]), finite_abs(v1[i])));
     }
-  }
+  };
+#pragma unroll 2
+  for (int row = r0 + tid / LPR; row < r1; row += RPP) measure(fetch(row), row);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     ak = fmaxf(ak, __shfl_xor_sync(0xffffffffu, ak, o));
@@ -288,10 +319,9 @@ __global__ void __launch_bounds__(kKvThreads) w4_kv_append_kernel(const __grid_c
     }
   }
   // the new rows (all lanes of a warp go round together: the row's lanes vote on NaNs)
-  for (int r = r0; r < r1; r += RPP) {
-    const int row = r + tid / LPR;
+  auto write = [&](const Raw& x, int row) {
     float k0[8], k1[8], v0[8], v1[8];
-    const bool live = row < r1 && fetch(row, k0, k1, v0, v1);
+    const bool live = row < r1 && open(x, row, k0, k1, v0, v1);
     bool nan = false;
     if (live) {
 #pragma unroll
@@ -302,14 +332,18 @@ __global__ void __launch_bounds__(kKvThreads) w4_kv_append_kernel(const __grid_c
       }
     }
     const uint32_t mask = __ballot_sync(0xffffffffu, nan);
-    if (!live) continue;
+    if (!live) return;
     uint2 c0 = codes8(k0, sk), c1 = codes8(k1, sk);
-    const uint32_t mine = ((1u << LPR) - 1u) << (lane / LPR * LPR);
-    if (mask & mine) c0 = c1 = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+    const uint32_t lanes = ((1u << LPR) - 1u) << (lane / LPR * LPR);
+    if (mask & lanes) c0 = c1 = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
     const uint2 d0 = codes8(v0, sv), d1 = codes8(v1, sv);
     *reinterpret_cast<uint2*>(kb + (long long)row * D + 8 * ck.c0) = c0;
     *reinterpret_cast<uint2*>(kb + (long long)row * D + 8 * ck.c1) = c1;
     *reinterpret_cast<uint4*>(vb + (long long)row * D + 16 * l) = make_uint4(d0.x, d0.y, d1.x, d1.y);
+  };
+  for (int r = r0; r < r1; r += RPP) {
+    const int row = r + tid / LPR;
+    write(row < r1 ? fetch(row) : Raw{}, row);
   }
 }
 
