@@ -39,8 +39,9 @@ namespace w4 {
 constexpr int kAtT = 32;                     // keys per unit
 constexpr int kAtWarps = 8;
 constexpr int kAtThreads = kAtWarps * 32;
-constexpr int kAtOv = 4;                     // what an item costs beside its units
+constexpr int kAtOv = 32;                    // what an item costs beside its units
 constexpr float kAtSlack = 6.f;
+constexpr int kAtMaxCtas = 160;              // CTAs of a launch, at most (pieces of an item)
 
 template <int D, int NT>
 struct AtSmem {
@@ -48,9 +49,11 @@ struct AtSmem {
   static constexpr int kStages = NT <= 2 ? 3 : 2;        // per warp
   static constexpr int kRows = 8 * NT;
   static constexpr int kRing = kAtWarps * kStages * kStage;
-  static constexpr int kMerge0 = kAtWarps / 2 * kRows * D * 4;   // half of the warps' sums
-  static constexpr int kPrefix = (W4_MAX_SEQS + 1) * 4;          // the split's prefix sums, before any merge
-  static constexpr int kMerge = kMerge0 > kPrefix ? kMerge0 : ((kPrefix + 15) & ~15);
+  // one place for the split's prefix sums, then half of the warps' sums, and the pieces' (maximum, sum)
+  static constexpr int kSums = kAtWarps / 2 * kRows * D * 4;
+  static constexpr int kPrefix = (W4_MAX_SEQS + 1 + 3) / 4 * 16;
+  static constexpr int kPieces = kAtMaxCtas * kRows * 8;
+  static constexpr int kMerge = kSums > kPrefix ? (kSums > kPieces ? kSums : kPieces) : (kPrefix > kPieces ? kPrefix : kPieces);
   static constexpr int oMerge = kRing;
   static constexpr int oM = oMerge + kMerge;             // [warps][rows] maxima
   static constexpr int oL = oM + kAtWarps * kRows * 4;   // [warps][rows] sums
@@ -490,28 +493,59 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
       __syncthreads();
       if (*flag) {
         __threadfence();
+        // maxima and sums of all pieces at once, a warp per row for the common maximum and the weights,
+        // then 16 pieces' sums in flight per thread
+        const int np = c1 - c0 + 1;
+        float2* pml = reinterpret_cast<float2*>(merge);              // [piece][row]
+        auto piece = [&](int k) { return slots + SLOT * (2 * (c0 + k) + (k == 0 ? 1 : 0)); };
+        for (int e = tid; e < np * R; e += kAtThreads) {
+          const float* s = piece(e / R) + (size_t)R * D + e % R;
+          pml[e] = make_float2(__ldcg(s), __ldcg(s + R));
+        }
+        __syncthreads();
+        for (int row = warp; row < R; row += kAtWarps) {
+          float mm = -INFINITY, ll = 0.f;
+          for (int k = lane; k < np; k += 32) mm = fmaxf(mm, pml[k * R + row].x);
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+          const float base = mm == -INFINITY ? 0.f : mm;
+          for (int k = lane; k < np; k += 32) {
+            const float2 x = pml[k * R + row];
+            const float f = attn_ex2(x.x - base);
+            ll = fmaf(x.y, f, ll);
+            pml[k * R + row].x = f;
+          }
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
+          if (lane == 0) {
+            sm[row] = mm;
+            sl[row] = ll;
+          }
+        }
+        __syncthreads();
         for (int e = tid; e < R * (D / 4); e += kAtThreads) {
           const int row = e / (D / 4), ch = e % (D / 4);
           if (row >= it.n * p.group) continue;
-          float mm = -INFINITY;
-          for (int c = c0; c <= c1; ++c)
-            mm = fmaxf(mm, __ldcg(slots + SLOT * (2 * c + (c == c0 ? 1 : 0)) + (size_t)R * D + row));
-          const float base = mm == -INFINITY ? 0.f : mm;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          float ll = 0.f;
-#pragma unroll 4
-          for (int c = c0; c <= c1; ++c) {
-            const float* s = slots + SLOT * (2 * c + (c == c0 ? 1 : 0));
-            const float f = attn_ex2(__ldcg(s + (size_t)R * D + row) - base);
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(s + (size_t)row * D + 4 * ch));
-            v.x = fmaf(y.x, f, v.x);
-            v.y = fmaf(y.y, f, v.y);
-            v.z = fmaf(y.z, f, v.z);
-            v.w = fmaf(y.w, f, v.w);
-            ll = fmaf(__ldcg(s + (size_t)R * D + R + row), f, ll);
+          for (int k0 = 0; k0 < np; k0 += 16) {
+            float4 y[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (k0 + k < np) y[k] = __ldcg(reinterpret_cast<const float4*>(piece(k0 + k) + (size_t)row * D + 4 * ch));
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float f = k0 + k < np ? pml[(k0 + k) * R + row].x : 0.f;
+              v.x = fmaf(y[k].x, f, v.x);
+              v.y = fmaf(y[k].y, f, v.y);
+              v.z = fmaf(y[k].z, f, v.z);
+              v.w = fmaf(y[k].w, f, v.w);
+            }
           }
-          store(row, ch, v, mm, ll);
+          store(row, ch, v, sm[row], sl[row]);
         }
+        __syncthreads();                             // the next item's maxima go to the same places
         if (tid == 0) *ticket = 0;
       }
     }
@@ -538,7 +572,8 @@ static cudaError_t launch_attn_nt(AtParams& p, cudaStream_t stream) {
   if (ea != cudaSuccess) return ea;
   static_assert(AtSmem<D, NT>::kTotal <= 227 * 1024, "shared memory of one CTA");
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)device_sm_count());
+  const int sms = device_sm_count();
+  cfg.gridDim = dim3((unsigned)(sms < kAtMaxCtas ? sms : kAtMaxCtas));
   cfg.blockDim = dim3(kAtThreads);
   cfg.dynamicSmemBytes = AtSmem<D, NT>::kTotal;
   cfg.stream = stream;
