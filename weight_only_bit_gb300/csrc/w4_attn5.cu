@@ -23,8 +23,9 @@
 //   warps 8-11       codes from global memory, FP16 into shared memory: keys in the canonical K-major
 //                    layout, values in the MN-major one (channels contiguous, as they lie in
 //                    memory: nothing is transposed).  A tile's loads are issued a tile ahead.
-//   warp 12          issues the MMAs: PV of a stream, then its next S, alternating between streams (the
-//                    whole warp walks, one elected lane issues: descriptors stay in uniform registers)
+//   warps 12, 13     issue the MMAs of stream 0 and 1: PV, then the next S in its place (the whole warp walks,
+//                    one elected lane issues: descriptors stay in uniform registers).  One warp for both
+//                    streams spent as long on waits and commits as the products take.
 // What bounds it: figures beside the launch below.
 #include <cstdint>
 #include <cuda.h>
@@ -42,7 +43,7 @@ namespace w4 {
 constexpr int kA5T = 128;                    // keys per tile
 constexpr int kA5R = 256;                    // rows per item, at most
 constexpr int kA5Ov = 2;                     // what an item costs beside its tiles
-constexpr int kA5Mma = 12;                   // the issuing warp
+constexpr int kA5Mma = 12;                   // the issuing warps: 12 and 13
 constexpr int kA5Threads = 512;
 // Registers a thread: launched with 128 each (65536 in all); 2 x 128 x 152 + 128 x 128 + 128 x 80 = 65536.
 constexpr int kA5RegsSoftmax = 152, kA5RegsMma = 80;
@@ -63,6 +64,11 @@ struct A5Smem {
   static constexpr int oPrefix = oFlag + 16;
   static constexpr int oOut = (oPrefix + (W4_MAX_SEQS + 1) * 4 + 15) & ~15;   // 8 softmax warps x 32 rows x 64 bytes
   static constexpr int kTotal = oOut + 8 * 2048 + 1024;
+};
+
+template <int S>
+struct A5Stream {
+  static constexpr int value = S;
 };
 
 struct A5Params {
@@ -204,7 +210,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
   uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + S::oBar);   // 4 decoding warps
-  uint64_t* kempty = kfull + 2;                                   // commit
+  uint64_t* kempty = kfull + 2;                                   // 2 commits
   uint64_t* vfull = kempty + 2;
   uint64_t* vempty = vfull + 2;
   uint64_t* scfull = vempty + 2;                                  // 4 decoding warps
@@ -222,9 +228,9 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&kfull[i], 4);
-      mbar_init(&kempty[i], 1);
+      mbar_init(&kempty[i], 2);
       mbar_init(&vfull[i], 4);
-      mbar_init(&vempty[i], 1);
+      mbar_init(&vempty[i], 2);
       mbar_init(&qfull[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
@@ -233,7 +239,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
       mbar_init(&pvdone[i], 1);
     }
     for (int i = 0; i < kA5ScaleSlots; ++i) mbar_init(&scfull[i], 4);
-    mbar_init(done, 1);
+    mbar_init(done, 2);
     *bad = 0;
     fence_mbar_init();
   }
@@ -359,64 +365,77 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
     } else if (warp >= kA5Mma) {
       // ================================================================ MMA issuer
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kA5RegsMma));
-      if (warp == kA5Mma) {
+      // The stream is a constant in each warp's code: descriptors that depend on the warp's index came out
+      // of the compiler wrong (rows of q read shifted), constants and uniform values do not.
+      auto issue = [&](auto stream) {
+        constexpr int s = decltype(stream)::value;
         constexpr uint32_t id_s = a5_idesc(64, false), id_o = a5_idesc(D, true);
         const uint32_t lead = a5_elect();
-        const uint64_t dq = a5_desc_k(sb + S::oQ), dk = a5_desc_k(sb + S::oK), dv = a5_desc_mn(sb + S::oV);
         constexpr uint64_t kStep = S::kTile >> 4;    // from a stage, or a stream's q, to the next
-        int items = 0;
-        uint32_t turn = 0;                           // parity of pfull, a bit per stream
+        const uint64_t dq = a5_desc_k(sb + S::oQ) + s * kStep, dk = a5_desc_k(sb + S::oK), dv = a5_desc_mn(sb + S::oV);
+        const uint32_t tms = tmem + s * 128, tmo = tmem + 256 + s * D;
+        uint32_t items = 0, turn = 0;                // parities of qfull and pfull
         bool more = true;
         while (more && ok) {
-          const int n = w.u1 - w.u0, tb = w.base;
+          const int n = w.u1 - w.u0;
           const bool two = w.it.n - w.it.rb * tpb > p.tpt;
-          // jobs of 64 keys: (tile, half, stream) with two row tiles, else (tile, half) and the tiles in turn
-          const int nq = two ? 4 * n : 2 * n;
-          const int last = two ? 3 : 1;              // the jobs of a tile, less one
-          ok = mbar_wait(&qfull[0], items & 1, 0x523) && mbar_wait(&qfull[1], items & 1, 0x524);
-          auto qk = [&](int q) {
-            const int s = two ? q & 1 : (q >> 1) & 1, h = two ? (q >> 1) & 1 : q & 1, tile = tb + (two ? q >> 2 : q >> 1);
-            if ((q & last) == 0) ok = ok && mbar_wait(&kfull[tile & 1], (tile >> 1) & 1, 0x525);
+          const int nj = two ? n : (n - s + 1) / 2;  // tiles of this stream: all, or every second
+          const int step = two ? 1 : 2;
+          if (nj > 0) {
+            ok = mbar_wait(&qfull[s], items, 0x523);
+            items ^= 1;
+          }
+          // S of half h of a tile; the tile's keys are free after the second
+          auto qk = [&](int tile, int h) {
+            const uint32_t st = tile & 1;
+            if (h == 0) ok = ok && mbar_wait(&kfull[st], (tile >> 1) & 1, 0x525);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
             t5_fence_after();
-            const uint64_t qa = dq + s * kStep, ka = dk + (tile & 1) * kStep + ((h * 64 * 128) >> 4);
+            const uint64_t ka = dk + st * kStep + ((h * 64 * 128) >> 4);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint64_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-              a5_mma_ss(lead, tmem + s * 128 + h * 64, qa + off, ka + off, id_s, k > 0 ? 1u : 0u);
+              a5_mma_ss(lead, tms + h * 64, dq + off, ka + off, id_s, k > 0 ? 1u : 0u);
             }
             a5_commit(lead, &sfull[2 * s + h]);
-            if ((q & last) == last) a5_commit(lead, &kempty[tile & 1]);
+            if (h == 1) {
+              a5_commit(lead, &kempty[st]);
+              if (!two) a5_commit(lead, &kempty[st]);
+            }
           };
-          auto pv = [&](int q) {
-            const int s = two ? q & 1 : (q >> 1) & 1, h = two ? (q >> 1) & 1 : q & 1, tile = tb + (two ? q >> 2 : q >> 1);
-            if ((q & last) == 0) ok = ok && mbar_wait(&vfull[tile & 1], (tile >> 1) & 1, 0x526);
-            ok = ok && mbar_wait(&pfull[2 * s + h], (turn >> s) & 1, 0x527);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) return;
-            if (h == 1) turn ^= 1u << s;
-            t5_fence_after();
-            const uint64_t va = dv + (tile & 1) * kStep + ((h * 64 * 128) >> 4);
-            const bool fresh = h == 0 && q < 4;      // the stream's first job of the item
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              a5_mma_ts(lead, tmem + 256 + s * D, tmem + s * 128 + h * 64 + k * 8, va + ((k * 2048) >> 4), id_o,
-                        (!fresh || k > 0) ? 1u : 0u);
-            a5_commit(lead, &pvdone[2 * s + h]);
-            if ((q & last) == last) a5_commit(lead, &vempty[tile & 1]);
-          };
-          for (int q = 0; q < 4 && q < nq && ok; ++q) qk(q);
-          for (int q = 0; q < nq && ok; ++q) {
-            pv(q);
-            if (ok && q + 4 < nq) qk(q + 4);
+          int tile = w.base + (two ? 0 : s);
+          if (nj > 0) {
+            qk(tile, 0);
+            if (ok) qk(tile, 1);
           }
-          ++items;
+          for (int j = 0; j < nj && ok; ++j, tile += step) {
+            const uint32_t st = tile & 1;
+            ok = mbar_wait(&vfull[st], (tile >> 1) & 1, 0x526);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              ok = ok && mbar_wait(&pfull[2 * s + h], turn, 0x527);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              t5_fence_after();
+              const uint64_t va = dv + st * kStep + ((h * 64 * 128) >> 4);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                a5_mma_ts(lead, tmo, tms + h * 64 + k * 8, va + ((k * 2048) >> 4), id_o, (j > 0 || h > 0 || k > 0) ? 1u : 0u);
+              a5_commit(lead, &pvdone[2 * s + h]);
+              if (j + 1 < nj) qk(tile + step, h);
+            }
+            turn ^= 1;
+            a5_commit(lead, &vempty[st]);
+            if (!two) a5_commit(lead, &vempty[st]);
+          }
           more = w.next(a, tpb);
         }
         a5_commit(lead, done);                       // nothing in flight when tensor memory is freed
         mbar_wait(done, 0, 0x528);
-      }
+      };
+      if (warp == kA5Mma) issue(A5Stream<0>{});
+      if (warp == kA5Mma + 1) issue(A5Stream<1>{});
     } else {
       // ================================================================ softmax
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kA5RegsSoftmax));
@@ -427,11 +446,15 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
       const int tok = tr / p.group, head = tr - tok * p.group;   // in the row tile
       int jobs = 0;
       bool more = true, asked = false;               // asked: this item's q is on its way
-      auto ask_q = [&](const Item& x) {
-        if (tr == 0) {
+      // (a stream without a tile of the item asks for nothing: the copy could land on the sums that go
+      // through q's places at the end)
+      auto ask_q = [&](const Walk<kA5T, kA5Ov>& y) {
+        const Item& x = y.it;
+        const bool both = x.n - x.rb * tpb > p.tpt;
+        if (tr == 0 && (both || y.u1 - y.u0 > s)) {
           a5_fence_proxy();                                      // the places may have held sums of an item
           mbar_arrive_expect_tx(&qfull[s], (uint32_t)(p.tpt * p.group * D * 2));
-          const int t0 = x.start + x.rb * tpb + (x.n - x.rb * tpb > p.tpt ? s * p.tpt : 0);
+          const int t0 = x.start + x.rb * tpb + (both ? s * p.tpt : 0);
 #pragma unroll
           for (int b = 0; b < D / 64; ++b)
             a5_tma3(sb + S::oQ + s * S::kTile + b * 16384, &p.tq, 64 * b, x.h * p.group, t0, &qfull[s]);
@@ -442,7 +465,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         const bool two = it.n - it.rb * tpb > p.tpt;
         const int i0 = it.rb * tpb + (two ? s * p.tpt : 0);      // the row tile's first token
         const int n = w.u1 - w.u0;
-        if (!asked) ask_q(w.it);
+        if (!asked) ask_q(w);
         asked = false;
         const int qi = i0 + tok;                                 // this row's token in the sequence
         const bool valid = tok < p.tpt && qi < it.n;
@@ -469,7 +492,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
             // the item's products with q are complete: the next item's rows may come in
             Walk<kA5T, kA5Ov> nx = w;
             if (nx.next(a, tpb)) {
-              ask_q(nx.it);
+              ask_q(nx);
               asked = true;
             }
           }
