@@ -11,10 +11,10 @@
 // An item has up to two row tiles, each with its own S, O and softmax warpgroup ("streams").  An item
 // of one row tile gives both streams the same rows and every second key tile each, joined at the
 // end; so the two softmax warpgroups always overlap the other's products.
-// Tensor memory is full: S 2 x 128 columns, O 2 x D columns (256 at D = 128); the weights P go back
-// over the first half of their S as FP16, the A operand of the second product.  A stream's S is two
-// halves of 64 keys with barriers of their own: while the softmax warps turn one half into weights, the
-// tensor cores multiply the other half's weights and fill it again.
+// Work goes in jobs of 64 keys (half a key tile).  Tensor memory is full: S 2 x 64 columns, the weights P
+// 2 x 2 x 32 (FP16, the A operand of the second product; two places per stream), O 2 x D (256 at
+// D = 128).  P has places of its own, not those of S: as soon as a job's S is in registers, the next
+// one's product runs, beside the exponentials.
 // Roles (four warpgroups of 128 threads; registers move from the last to the first two), connected by
 // mbarriers:
 //   warps 0-3, 4-7   softmax of stream 0 and 1: a thread per row, one pass over its S, 64 keys at a time:
@@ -23,7 +23,7 @@
 //   warps 8-11       codes from global memory, FP16 into shared memory: keys in the canonical K-major
 //                    layout, values in the MN-major one (channels contiguous, as they lie in
 //                    memory: nothing is transposed).  A tile's loads are issued a tile ahead.
-//   warps 12, 13     issue the MMAs of stream 0 and 1: PV, then the next S in its place (the whole warp walks,
+//   warps 12, 13     issue the MMAs of stream 0 and 1: the next S, then PV (the whole warp walks,
 //                    one elected lane issues: descriptors stay in uniform registers).  One warp for both
 //                    streams spent as long on waits and commits as the products take.
 // What bounds it: figures beside the launch below.
@@ -59,7 +59,7 @@ struct A5Smem {
   static constexpr int oScales = 6 * kTile;              // [slots][8 groups] (ks c, log2 vs, 1 / vs, 0)
   static constexpr int oMl = oScales + kA5ScaleSlots * 8 * 16;   // [128] (maximum, sum) of stream 1
   static constexpr int oBar = oMl + 128 * 8;
-  static constexpr int kBars = 2 + 2 + 2 + 2 + kA5ScaleSlots + 4 + 4 + 2 + 4 + 1;
+  static constexpr int kBars = 2 + 2 + 2 + 2 + kA5ScaleSlots + 2 + 2 + 4 + 2 + 4 + 1;
   static constexpr int oFlag = oBar + kBars * 8;
   static constexpr int oPrefix = oFlag + 16;
   static constexpr int oOut = (oPrefix + (W4_MAX_SEQS + 1) * 4 + 15) & ~15;   // 8 softmax warps x 32 rows x 64 bytes
@@ -214,10 +214,11 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
   uint64_t* vfull = kempty + 2;
   uint64_t* vempty = vfull + 2;
   uint64_t* scfull = vempty + 2;                                  // 4 decoding warps
-  uint64_t* sfull = scfull + kA5ScaleSlots;                       // commit: S of (stream, half) is there
-  uint64_t* pfull = sfull + 4;                                    // 4 softmax warps: P of (stream, half) is there
+  uint64_t* sfull = scfull + kA5ScaleSlots;                       // commit: S of the stream is there
+  uint64_t* sfree = sfull + 2;                                    // 4 softmax warps: S is in registers
+  uint64_t* pfull = sfree + 2;                                    // 4 softmax warps: P of (stream, place) is there
   uint64_t* qfull = pfull + 4;                                    // TMA: Q of the stream is there
-  uint64_t* pvdone = qfull + 2;                                   // commit: O has taken in P of (stream, half)
+  uint64_t* pvdone = qfull + 2;                                   // commit: O has taken in P of (stream, place)
   uint64_t* done = pvdone + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::oFlag);
   int* flag = reinterpret_cast<int*>(smem + S::oFlag + 8);
@@ -232,9 +233,10 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
       mbar_init(&vfull[i], 4);
       mbar_init(&vempty[i], 2);
       mbar_init(&qfull[i], 1);
+      mbar_init(&sfull[i], 1);
+      mbar_init(&sfree[i], 4);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], 4);
       mbar_init(&pvdone[i], 1);
     }
@@ -373,8 +375,8 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         const uint32_t lead = a5_elect();
         constexpr uint64_t kStep = S::kTile >> 4;    // from a stage, or a stream's q, to the next
         const uint64_t dq = a5_desc_k(sb + S::oQ) + s * kStep, dk = a5_desc_k(sb + S::oK), dv = a5_desc_mn(sb + S::oV);
-        const uint32_t tms = tmem + s * 128, tmo = tmem + 256 + s * D;
-        uint32_t items = 0, turn = 0;                // parities of qfull and pfull
+        const uint32_t tms = tmem + s * 64, tmp = tmem + 128 + s * 64, tmo = tmem + 256 + s * D;
+        uint32_t items = 0, turn = 0;                // parities of qfull and, by tile, of pfull
         bool more = true;
         while (more && ok) {
           const int n = w.u1 - w.u0;
@@ -396,24 +398,26 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint64_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-              a5_mma_ss(lead, tms + h * 64, dq + off, ka + off, id_s, k > 0 ? 1u : 0u);
+              a5_mma_ss(lead, tms, dq + off, ka + off, id_s, k > 0 ? 1u : 0u);
             }
-            a5_commit(lead, &sfull[2 * s + h]);
+            a5_commit(lead, &sfull[s]);
             if (h == 1) {
               a5_commit(lead, &kempty[st]);
               if (!two) a5_commit(lead, &kempty[st]);
             }
           };
           int tile = w.base + (two ? 0 : s);
-          if (nj > 0) {
-            qk(tile, 0);
-            if (ok) qk(tile, 1);
-          }
+          if (nj > 0) qk(tile, 0);                   // (the last S before was read: its P came)
           for (int j = 0; j < nj && ok; ++j, tile += step) {
             const uint32_t st = tile & 1;
-            ok = mbar_wait(&vfull[st], (tile >> 1) & 1, 0x526);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+              // the next S, once this one is in registers (a tile has two jobs: the parity is the half)
+              if (h == 0 || j + 1 < nj) {
+                ok = ok && mbar_wait(&sfree[s], h, 0x524);
+                if (ok) qk(h == 0 ? tile : tile + step, h ^ 1);
+              }
+              if (h == 0) ok = ok && mbar_wait(&vfull[st], (tile >> 1) & 1, 0x526);
               ok = ok && mbar_wait(&pfull[2 * s + h], turn, 0x527);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
@@ -421,10 +425,10 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
               const uint64_t va = dv + st * kStep + ((h * 64 * 128) >> 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                a5_mma_ts(lead, tmo, tms + h * 64 + k * 8, va + ((k * 2048) >> 4), id_o, (j > 0 || h > 0 || k > 0) ? 1u : 0u);
+                a5_mma_ts(lead, tmo, tmp + h * 32 + k * 8, va + ((k * 2048) >> 4), id_o, (j > 0 || h > 0 || k > 0) ? 1u : 0u);
               a5_commit(lead, &pvdone[2 * s + h]);
-              if (j + 1 < nj) qk(tile + step, h);
             }
+            if (!ok) break;
             turn ^= 1;
             a5_commit(lead, &vempty[st]);
             if (!two) a5_commit(lead, &vempty[st]);
@@ -442,7 +446,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
       const int s = warp >> 2;
       const int tr = tid & 127;                      // row of the stream's tile = tensor-memory lane
       const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-      const uint32_t ts = tl + s * 128, to = tl + 256 + s * D;
+      const uint32_t ts = tl + s * 64, tp = tl + 128 + s * 64, to = tl + 256 + s * D;
       const int tok = tr / p.group, head = tr - tok * p.group;   // in the row tile
       int jobs = 0;
       bool more = true, asked = false;               // asked: this item's q is on its way
@@ -481,13 +485,13 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
           const int jt = w.base + tile;
           const int slot = jt & (kA5ScaleSlots - 1);
           if (ok && h == 0) ok = mbar_wait(&scfull[slot], (jt / kA5ScaleSlots) & 1, 0x529);
-          if (ok) ok = mbar_wait(&sfull[2 * s + h], (jobs >> 1) & 1, 0x52a);
+          if (ok) ok = mbar_wait(&sfull[s], h, 0x52a);           // two jobs a tile: the parity is the half
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           t5_fence_after();
           float x[64];
-          a5_ld32(ts + h * 64, *reinterpret_cast<float(*)[32]>(&x[0]));
-          a5_ld32(ts + h * 64 + 32, *reinterpret_cast<float(*)[32]>(&x[32]));
+          a5_ld32(ts, *reinterpret_cast<float(*)[32]>(&x[0]));
+          a5_ld32(ts + 32, *reinterpret_cast<float(*)[32]>(&x[32]));
           if (two && q == 2 * nj - 1) {
             // the item's products with q are complete: the next item's rows may come in
             Walk<kA5T, kA5Ov> nx = w;
@@ -504,6 +508,9 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
           for (int g = 0; g < 4; ++g) sc[g] = a5_lds_f4(ssc + g * 16);
           a5_wait32(*reinterpret_cast<float(*)[32]>(&x[0]));
           a5_wait32(*reinterpret_cast<float(*)[32]>(&x[32]));
+          t5_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfree[s]);
           // a warp whose rows all see all keys (nearly every one) tests none
           if (__any_sync(0xffffffffu, clo > 0 || chi < 64)) {
 #pragma unroll
@@ -566,7 +573,8 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
               }
               l = fmaf(sum.x + sum.y, f.z, l);
             }
-            a5_st16(ts + h * 64 + c * 16, pk);                   // over columns of S that have been read
+            // (the place is free: the P before the last was taken in ahead of this job's S)
+            a5_st16(tp + h * 32 + c * 16, pk);
           }
           a5_wait_st();
           t5_fence_before();
