@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
   // this warp's units: warp + 8 i of the CTA's tiles
 
   // ---- loading: lane (i, s) = (lane / 2, lane % 2) knows 16-key group s of unit 16 * batch + i
-  const int P = a.c.page;
+  const int P = a.c.page, lgp = 31 - __clz(P);       // a power of two
   const int sub = lane & 1;
   const int per = P >= kAtT ? 2 : 1;         // 16-key groups per box
   Walk<kAtT, kAtOv> ahead = w;               // walks with the batches: each lane to its own unit
@@ -171,12 +171,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
     if (left) {
       const int key = (ahead.it.t0 + ahead.u0 + unit - ahead.base) * kAtT + 16 * sub;
       if (key < ahead.it.hi && key + 16 > ahead.it.lo) {
-        const int page = __ldg(a.c.table + (long long)ahead.it.b * a.c.table_stride + key / P);
+        const int page = __ldg(a.c.table + (long long)ahead.it.b * a.c.table_stride + (key >> lgp));
         if (page < 0 || page >= a.c.num_pages) {
           attn_range_error(0x501);
         } else {
           g.page = page;
-          g.row = ahead.it.h * P + key % P / kAtT * kAtT;
+          g.row = ahead.it.h * P + ((key & (P - 1)) & ~(kAtT - 1));
           g.ks = __ldg(a.c.k_scale + (long long)page * a.c.scale_stride + ahead.it.h) * c2;
           const float vs = __ldg(a.c.v_scale + (long long)page * a.c.scale_stride + ahead.it.h);
           g.lvs = log2f(vs);
@@ -209,14 +209,35 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
   const int f0 = t + 4 * (t & 1), f1 = f0 ^ 4;       // keys of an 8-key group that weights 2t, 2t + 1 belong to
   // the key of A row g (and g + 8): perm = {0, 4, 5, 1, 2, 6, 7, 3}
   const int pg = (g & 1) ? ((g >> 1) + 4 * ((g >> 1) & 1)) ^ 4 : (g >> 1) + 4 * ((g >> 1) & 1);
+  // B column g of each tile is a row of q
+  uint32_t qf[NT][D / 16][2];
+  auto load_q = [&](const Item& x) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = n * 8 + g;
+      const bool valid = row < x.n * p.group;
+      const int tok = row / p.group;
+      const __half* q = a.q + (long long)(x.start + tok) * a.q_stride + (long long)(x.h * p.group + row - tok * p.group) * D;
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        uint2 v = make_uint2(0, 0);
+        if (valid) v = __ldg(reinterpret_cast<const uint2*>(q + 16 * (t + 4 * (s >> 2)) + 4 * (s & 3)));
+        qf[n][s][0] = v.x;
+        qf[n][s][1] = v.y;
+      }
+    }
+  };
+  // (more row tiles leave no registers for the next item's)
+  constexpr bool kEarly = NT <= 2;
+  if (kEarly) load_q(w.it);
   int i = 0;                                         // this warp's units so far
   bool ok = true, more = true;
   while (more) {
     const Item& it = w.it;
+    if (!kEarly) load_q(it);
     const int shift = it.total - it.n;
-    // columns 2t and 2t + 1 of each tile are rows of q: the keys [rlo, rhi) that they see
+    // columns 2t and 2t + 1 of each tile: the keys [rlo, rhi) that they see
     int rlo[NT][2], rhi[NT][2];
-    uint32_t qf[NT][D / 16][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -225,16 +246,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
         const int pos = row < it.n * p.group ? shift + row / p.group : -1;
         rhi[n][e] = pos < 0 ? 0 : a.causal ? min(it.total, pos + 1) : it.total;
         rlo[n][e] = a.window > 0 ? pos - a.window + 1 : 0;
-      }
-      const int row = n * 8 + g;                     // B column g
-      const bool valid = row < it.n * p.group;
-      const __half* q = a.q + (long long)(it.start + row / p.group) * a.q_stride + (long long)(it.h * p.group + row % p.group) * D;
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        uint2 v = make_uint2(0, 0);
-        if (valid) v = __ldg(reinterpret_cast<const uint2*>(q + 16 * (t + 4 * (s >> 2)) + 4 * (s & 3)));
-        qf[n][s][0] = v.x;
-        qf[n][s][1] = v.y;
       }
     }
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
@@ -384,6 +395,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
       if ((i & 15) == 15) cur = nxt;
     }
 
+    // the next item's rows of q, on their way during the join
+    Walk<kAtT, kAtOv> after = w;
+    more = after.next(a, a.max_q);
+    if (kEarly && more) load_q(after.it);
     // ---------------------------------------------------------------- join the warps
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -549,7 +564,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
         if (tid == 0) *ticket = 0;
       }
     }
-    more = w.next(a, a.max_q);
+    w = after;
   }
   if (!ok) {                                         // a lost wait: the copies in flight must land all the same
     for (int k = i; k < i + NST; ++k) mbar_wait(&full[k % NST], (k / NST) & 1, 0x519);

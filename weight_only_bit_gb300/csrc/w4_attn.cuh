@@ -155,7 +155,8 @@ struct Walk {
     it.h = (begin - prefix[lo]) / per;
     at = prefix[lo] + it.h * per;
     // the token block: scan of the blocks' costs, 32 at a time
-    for (int r0 = 0;; r0 += 32) {
+    if (blocks == 1) item_block<T>(a, it, tpb, 0);
+    else for (int r0 = 0;; r0 += 32) {
       int u = 0;
       if (r0 + lane < blocks) {
         item_block<T>(a, it, tpb, r0 + lane);

@@ -39,8 +39,8 @@ struct VerifyPlan {
 
 static VerifyPlan plan_verify(int batch, int rows, int vocab, int sms) {
   VerifyPlan p;
-  // about eight CTAs per SM, at least 4096 tokens each (16 a thread)
-  const long long want = 8LL * sms;
+  // about sixteen CTAs per SM (four run at once), at least 4096 tokens each (16 a thread)
+  const long long want = 16LL * sms;
   auto cut = [&](long long n, int most) {
     long long k = want / n;
     const long long fit = (vocab + 4095) / 4096;
@@ -52,7 +52,7 @@ static VerifyPlan plan_verify(int batch, int rows, int vocab, int sms) {
   p.pieces = cut((long long)batch * rows, kVfMaxPieces);
   p.piece = (vecs + p.pieces - 1) / p.pieces;
   p.pieces = (vecs + p.piece - 1) / p.piece;
-  p.parts = cut(2LL * batch, kVfMaxParts);
+  p.parts = cut(4LL * batch, kVfMaxParts);
   p.part = ((vocab + p.parts - 1) / p.parts + 7) & ~7;
   p.parts = (vocab + p.part - 1) / p.part;
   return p;
@@ -148,6 +148,21 @@ __device__ __forceinline__ unsigned long long vf_warp_max(unsigned long long k) 
   return k;
 }
 
+// Two FP32 operations in one instruction.
+__device__ __forceinline__ float2 vf_fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 vf_add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 // Joins two (reference, sum) pairs.
 __device__ __forceinline__ float2 vf_join(float2 a, float2 b) {
   const float m = fmaxf(a.x, b.x);
@@ -209,15 +224,14 @@ __global__ void __launch_bounds__(kVfThreads) w4_verify_stats_kernel(const __gri
         sum *= vf_ex2(m - mx * c);           // 0 where there was nothing
         m = mx * c;
       }
-      const float z = m == -INFINITY ? 0.f : m;
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      const float2 z = make_float2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m), cc = make_float2(c, c);
+      float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float2 f = vf_pair(u[i]);
-        s[(2 * i) & 3] += vf_ex2(fmaf(f.x, c, -z));
-        s[(2 * i + 1) & 3] += vf_ex2(fmaf(f.y, c, -z));
+        const float2 e = vf_fma2(vf_pair(u[i]), cc, z);
+        s[i & 1] = vf_add2(s[i & 1], make_float2(vf_ex2(e.x), vf_ex2(e.y)));
       }
-      return (s[0] + s[1]) + (s[2] + s[3]);
+      return (s[0].x + s[0].y) + (s[1].x + s[1].y);
     };
     const float t0 = top, m0 = m, s0 = sum;
     const int at0 = at;
@@ -235,13 +249,7 @@ __global__ void __launch_bounds__(kVfThreads) w4_verify_stats_kernel(const __gri
     }
     sum += s;
   };
-  for (int k = piece * pl.piece + tid; k < k1; k += kVfThreads * 4) {
-    uint4 w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[i] = make_uint4(0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u);
-      if (k + i * kVfThreads < k1) w[i] = ld_nc_v4(base + 8 * (size_t)(k + i * kVfThreads));
-    }
+  auto sums = [&](const uint4 (&w)[4], int k) {
     uint32_t u[16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -251,6 +259,34 @@ __global__ void __launch_bounds__(kVfThreads) w4_verify_stats_kernel(const __gri
       u[4 * i + 3] = w[i].w;
     }
     take(u, k);
+  };
+  // rounds of four vectors a thread, the next round's loads in flight beside the sums of this one
+  const __half* at8 = base + 8 * (size_t)(piece * pl.piece + tid);
+  int k = piece * pl.piece;
+  const int rounds = max(k1 - k, 0) / (kVfThreads * 4);
+  uint4 w[4];
+  if (rounds > 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = ld_nc_v4(at8 + i * kVfThreads * 8);
+  }
+  for (int r = 1; r <= rounds; ++r, k += kVfThreads * 4) {
+    uint4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = w[i];
+    at8 += kVfThreads * 32;
+    if (r < rounds) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = ld_nc_v4(at8 + i * kVfThreads * 8);
+    }
+    sums(x, k + tid);
+  }
+  if (k < k1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = make_uint4(0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u);
+      if (k + tid + i * kVfThreads < k1) w[i] = ld_nc_v4(at8 + i * kVfThreads * 8);
+    }
+    sums(w, k + tid);
   }
   unsigned long long key = GREEDY ? vf_key(top, at) : 0;
   if (piece == 0) {
