@@ -1,0 +1,172 @@
+"""Draft-and-verify decoding on 4-bit weights: the projections, the paged 8-bit cache, the attention over it
+and the verification of drafted tokens, together.
+
+A synthetic model of the decode step's shapes (synth.DECODE_SHAPES: 12 query and 2 key/value heads of
+128 channels, random weights quantised by libw4) generates from a prompt.  Each step feeds the last token
+and up to `drafts` tokens that follow an earlier occurrence of the last two tokens in the context
+("prompt lookup"), appends their keys and values to the cache (w4_kv_append), attends (w4_attn_kv8),
+and lets w4_spec_verify keep the drafted tokens that the model's own probabilities allow.  The cache
+forgets the others by their length alone: kv_len shrinks, the next append writes over them.
+
+    python -m weight_only_bit_gb300.serve --layers 2 --tokens 48
+
+Norms, residuals, the gate's SiLU and the embedding are plain torch operations; they are not part of
+libw4.
+"""
+from __future__ import annotations
+
+import weight_only_bit_gb300 as w4
+
+from . import synth
+from .step import DecodeStep
+
+Q_HEADS, KV_HEADS, HEAD_DIM = 12, 2, 128
+
+
+class Server:
+    """One sequence.  `capacity`: tokens that the cache holds; `drafts`: most drafted tokens a step."""
+
+    def __init__(self, fmt: str = "nf4", layers: int = 2, capacity: int = 2048, page_tokens: int = 64, drafts: int = 4,
+                 temperature: float = 0.0, seed: int = 0, device: str = "cuda:0"):
+        import torch
+        self.torch, self.dev = torch, torch.device(device)
+        self.layers, self.drafts, self.temperature, self.page = layers, drafts, temperature, page_tokens
+        # the weights of a decode step of so many layers, quantised on the GPU
+        st = DecodeStep(fmt, 1, device, layers=layers).build()
+        self.format, self.bs, self.code = st.format, st.bs, st.code
+        self.weights = {(layer, proj): (st.packed[i], st.scales[i], n, k) for i, (layer, proj, n, k) in enumerate(st.gemvs)}
+        self.head = next(key for key in self.weights if key[1] == "lm_head")
+        self.vocab, self.dim = self.weights[self.head][2:]
+        self.gen = torch.Generator(device=self.dev)
+        self.gen.manual_seed(seed)
+        self.embed = torch.randn((self.vocab, self.dim), generator=self.gen, device=self.dev, dtype=torch.float16)
+        # a pool of pages per layer, one page table: page i of the sequence is page i of every pool
+        pages = -(-capacity // page_tokens)
+        self.capacity = pages * page_tokens
+        self.table = torch.arange(pages, dtype=torch.int32, device=self.dev).reshape(1, -1)
+        shape = (pages, KV_HEADS, page_tokens, HEAD_DIM)
+        self.caches = []
+        for _ in range(layers):
+            k, v = (torch.zeros(shape, dtype=torch.uint8, device=self.dev) for _ in range(2))
+            ks, vs = (torch.ones((pages, KV_HEADS), device=self.dev) for _ in range(2))
+            self.caches.append(w4.w4_kv_cache(k, v, ks, vs, self.table, num_pages=pages, kv_heads=KV_HEADS,
+                                              page_tokens=page_tokens, head_dim=HEAD_DIM, table_stride=pages))
+        ang = torch.arange(self.capacity, dtype=torch.float64)[:, None] * \
+            1e6 ** (-torch.arange(0, HEAD_DIM, 2, dtype=torch.float64) / HEAD_DIM)
+        self.cos, self.sin = ang.cos().float().to(self.dev), ang.sin().float().to(self.dev)
+        self.attn_ws = torch.zeros(w4.w4_attn_workspace_bytes(self.capacity, 1, Q_HEADS, KV_HEADS, HEAD_DIM),
+                                   dtype=torch.uint8, device=self.dev)
+        self.verify_ws = torch.zeros(w4.w4_spec_verify_workspace_bytes(1, max(drafts, 1), self.vocab), dtype=torch.uint8,
+                                     device=self.dev)
+        self.context, self.cached = [], 0            # tokens so far; how many of them are in the cache
+        self.steps = self.accepted = 0
+
+    # ------------------------------------------------------------------ the model
+    def _gemv(self, layer, proj, x):
+        packed, scales, n, k = self.weights[(layer, proj)]
+        y = self.torch.empty((x.shape[0], n), dtype=self.torch.float16, device=self.dev)
+        w4.check(w4.w4_gemv_sequence([dict(format=self.format, packed=packed, scales=scales, codebook=self.code, x=x, y=y,
+                                           M=x.shape[0], N=n, K=k, blocksize=self.bs)]), proj)
+        return y
+
+    def _norm(self, h):
+        h = h.float()
+        return (h * self.torch.rsqrt(h.square().mean(-1, keepdim=True) + 1e-6)).half()
+
+    def forward(self, tokens):
+        """Logits [len(tokens), vocab] of tokens at the positions after the cached ones; they are cached."""
+        torch, n = self.torch, len(tokens)
+        total = self.cached + n
+        if total > self.capacity:
+            raise w4.W4Error(w4.W4_ERR_LIMIT, f"{total} tokens in a cache of {self.capacity}")
+        q_start = torch.tensor([0, n], dtype=torch.int32, device=self.dev)
+        kv_len = torch.tensor([total], dtype=torch.int32, device=self.dev)
+        h = self.embed[torch.tensor(tokens, device=self.dev)].float()
+        for layer, cache in enumerate(self.caches):
+            x = self._norm(h)
+            q, k, v = (self._gemv(layer, p, x) for p in ("q", "k", "v"))
+            w4.check(w4.w4_kv_append(cache, q, k, v, q, self.cos, self.sin, q_start, kv_len, n, 1, Q_HEADS, n, self.capacity,
+                                     HEAD_DIM), "append")
+            o = torch.empty_like(q)
+            w4.check(w4.w4_attn_kv8(cache, q, o, None, q_start, kv_len, n, 1, Q_HEADS, n, HEAD_DIM ** -0.5, self.attn_ws),
+                     "attention")
+            h = h + self._gemv(layer, "o", o).float()
+            x = self._norm(h)
+            gate, up = self._gemv(layer, "gate", x).float(), self._gemv(layer, "up", x).float()
+            h = h + self._gemv(layer, "down", (gate * torch.sigmoid(gate) * up).half()).float()
+        self.cached = total
+        return self._gemv(*self.head, self._norm(h))
+
+    # ------------------------------------------------------------------ the loop
+    def lookup(self):
+        """Up to `drafts` tokens that followed the latest earlier occurrence of the last two."""
+        c = self.context
+        for i in range(len(c) - 3, -1, -1):
+            if c[i:i + 2] == c[-2:]:
+                return c[i + 2:i + 2 + self.drafts]
+        return []
+
+    def prefill(self, prompt):
+        """Caches all tokens of the prompt but the last, which the first step feeds."""
+        self.context = list(prompt)
+        if len(prompt) > 1:
+            self.forward(self.context[:-1])
+
+    def step(self):
+        """One draft-and-verify step; returns the new tokens (the accepted drafts and one more)."""
+        torch = self.torch
+        drafted = self.lookup()
+        n = max(len(drafted), 1)                     # the operator takes at least one place; n_drafts says how many count
+        before = self.cached
+        logits = self.forward([self.context[-1]] + drafted)
+        target = logits if drafted else torch.cat([logits, logits])
+        i32 = dict(dtype=torch.int32, device=self.dev)
+        tokens, accepted = torch.empty((1, n + 1), **i32), torch.empty((1,), **i32)
+        u = torch.rand((1, n), generator=self.gen, device=self.dev)
+        e = torch.empty((1, self.vocab), device=self.dev).exponential_(generator=self.gen).clamp_min_(1e-12)
+        w4.check(w4.w4_spec_verify(target, None, torch.tensor([drafted or [-1]], **i32), u, e, tokens, accepted, None, 1, n,
+                                   self.vocab, self.temperature, self.verify_ws,
+                                   n_drafts=torch.tensor([len(drafted)], **i32)), "verify")
+        new = [t for t in tokens[0].tolist() if t >= 0]
+        # the refused drafts' keys and values stay behind the length, to be written over
+        self.cached = before + len(new)
+        self.context += new
+        self.steps += 1
+        self.accepted += len(new) - 1
+        return new
+
+    def generate(self, prompt, count):
+        self.prefill(prompt)
+        out = []
+        while len(out) < count:
+            out += self.step()
+        w4.check(w4.w4_device_check())
+        return out[:count]
+
+
+def _main():
+    import argparse
+    import time
+    import torch
+    ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
+    ap.add_argument("--fmt", default="nf4", choices=["nf4", "int4", "fp4"])
+    ap.add_argument("--layers", type=int, default=2)
+    ap.add_argument("--prompt", type=int, default=300, help="tokens of the random prompt")
+    ap.add_argument("--tokens", type=int, default=48)
+    ap.add_argument("--drafts", type=int, default=4)
+    ap.add_argument("--temperature", type=float, default=0.0)
+    a = ap.parse_args()
+    from weight_only_bit_gb300 import build as _b
+    _b.build()
+    s = Server(a.fmt, a.layers, capacity=a.prompt + a.tokens + 64, drafts=a.drafts, temperature=a.temperature)
+    g = torch.Generator().manual_seed(1)
+    prompt = torch.randint(0, s.vocab, (a.prompt,), generator=g).tolist()
+    t = time.perf_counter()
+    out = s.generate(prompt, a.tokens)
+    dt = time.perf_counter() - t
+    print(f"{a.fmt}, {a.layers} layers, {a.prompt} + {len(out)} tokens: {s.steps} steps, {s.accepted} drafts accepted, {dt * 1e3:.1f} ms")
+    print("tokens:", out[:16], "..." if len(out) > 16 else "")
+
+
+if __name__ == "__main__":
+    _main()
