@@ -59,7 +59,7 @@ struct A5Smem {
   static constexpr int oScales = 6 * kTile;              // [slots][8 groups] (ks c, log2 vs, 1 / vs, 0)
   static constexpr int oMl = oScales + kA5ScaleSlots * 8 * 16;   // [128] (maximum, sum) of stream 1
   static constexpr int oBar = oMl + 128 * 8;
-  static constexpr int kBars = 2 + 2 + 2 + 2 + kA5ScaleSlots + 2 + 2 + 4 + 2 + 4 + 1;
+  static constexpr int kBars = 2 + 2 + 2 + 2 + 2 + 2 + 4 + 2 + 4 + 1;
   static constexpr int oFlag = oBar + kBars * 8;
   static constexpr int oPrefix = oFlag + 16;
   static constexpr int oOut = (oPrefix + (W4_MAX_SEQS + 1) * 4 + 15) & ~15;   // 8 softmax warps x 32 rows x 64 bytes
@@ -147,6 +147,29 @@ __device__ __forceinline__ float4 a5_lds_f4(uint32_t a) {
 __device__ __forceinline__ void a5_fence_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void a5_sync_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
+// A bounded wait like mbar_wait, without a suspend hint: a wait on a phase that is complete takes 90 cycles
+// and not 122, a hand-over between two warps 130 and not 160, and this kernel lives on hand-overs.
+__device__ __forceinline__ bool a5_try(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool a5_wait(uint32_t bar, uint32_t parity, uint32_t site) {
+  if (a5_try(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (a5_try(bar, parity)) return true;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+  }
+  atomicCAS(&g_error_word, 0u, site);
+  return false;
+}
+__device__ __forceinline__ void a5_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ void a5_tma3(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
@@ -213,8 +236,8 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
   uint64_t* kempty = kfull + 2;                                   // 2 commits
   uint64_t* vfull = kempty + 2;
   uint64_t* vempty = vfull + 2;
-  uint64_t* scfull = vempty + 2;                                  // 4 decoding warps
-  uint64_t* sfull = scfull + kA5ScaleSlots;                       // commit: S of the stream is there
+  uint64_t* sfull = vempty + 2;                                   // commit: S of the stream is there, and an arrival of
+                                                                  // the issuing warp: so are the keys' scales
   uint64_t* sfree = sfull + 2;                                    // 4 softmax warps: S is in registers
   uint64_t* pfull = sfree + 2;                                    // 4 softmax warps: P of (stream, place) is there
   uint64_t* qfull = pfull + 4;                                    // TMA: Q of the stream is there
@@ -233,14 +256,13 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
       mbar_init(&vfull[i], 4);
       mbar_init(&vempty[i], 2);
       mbar_init(&qfull[i], 1);
-      mbar_init(&sfull[i], 1);
+      mbar_init(&sfull[i], 2);
       mbar_init(&sfree[i], 4);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&pfull[i], 4);
       mbar_init(&pvdone[i], 1);
     }
-    for (int i = 0; i < kA5ScaleSlots; ++i) mbar_init(&scfull[i], 4);
     mbar_init(done, 2);
     *bad = 0;
     fence_mbar_init();
@@ -350,10 +372,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
               make_float4(ks * c2, log2f(vs), __fdiv_rn(1.f, vs), 0.f);
         a5_fence_proxy();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&kfull[st]);
-          mbar_arrive(&scfull[j & (kA5ScaleSlots - 1)]);
-        }
+        if (lane == 0) mbar_arrive(&kfull[st]);
         if (j >= 2) ok = mbar_wait(&vempty[st], ((j >> 1) - 1) & 1, 0x522);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -376,24 +395,26 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         constexpr uint64_t kStep = S::kTile >> 4;    // from a stage, or a stream's q, to the next
         const uint64_t dq = a5_desc_k(sb + S::oQ) + s * kStep, dk = a5_desc_k(sb + S::oK), dv = a5_desc_mn(sb + S::oV);
         const uint32_t tms = tmem + s * 64, tmp = tmem + 128 + s * 64, tmo = tmem + 256 + s * D;
+        const uint32_t b_q = smem_u32(qfull + s), b_k = smem_u32(kfull), b_v = smem_u32(vfull), b_s = smem_u32(sfull + s),
+                       b_f = smem_u32(sfree + s), b_p = smem_u32(pfull + 2 * s);
         uint32_t items = 0, turn = 0;                // parities of qfull and, by tile, of pfull
         bool more = true;
-        while (more && ok) {
+        // (after a lost wait the walk goes on without waiting: the other warps' counts stay right)
+        while (more) {
           const int n = w.u1 - w.u0;
           const bool two = w.it.n - w.it.rb * tpb > p.tpt;
           const int nj = two ? n : (n - s + 1) / 2;  // tiles of this stream: all, or every second
           const int step = two ? 1 : 2;
           if (nj > 0) {
-            ok = mbar_wait(&qfull[s], items, 0x523);
+            ok = ok && a5_wait(b_q, items, 0x523);
             items ^= 1;
           }
           // S of half h of a tile; the tile's keys are free after the second
           auto qk = [&](int tile, int h) {
             const uint32_t st = tile & 1;
-            if (h == 0) ok = ok && mbar_wait(&kfull[st], (tile >> 1) & 1, 0x525);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) return;
+            if (h == 0) ok = ok && a5_wait(b_k + st * 8, (tile >> 1) & 1, 0x525);
             t5_fence_after();
+            __syncwarp();
             const uint64_t ka = dk + st * kStep + ((h * 64 * 128) >> 4);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
@@ -401,6 +422,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
               a5_mma_ss(lead, tms, dq + off, ka + off, id_s, k > 0 ? 1u : 0u);
             }
             a5_commit(lead, &sfull[s]);
+            if (lane == 0) a5_arrive(b_s);
             if (h == 1) {
               a5_commit(lead, &kempty[st]);
               if (!two) a5_commit(lead, &kempty[st]);
@@ -408,27 +430,25 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
           };
           int tile = w.base + (two ? 0 : s);
           if (nj > 0) qk(tile, 0);                   // (the last S before was read: its P came)
-          for (int j = 0; j < nj && ok; ++j, tile += step) {
+          for (int j = 0; j < nj; ++j, tile += step) {
             const uint32_t st = tile & 1;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               // the next S, once this one is in registers (a tile has two jobs: the parity is the half)
               if (h == 0 || j + 1 < nj) {
-                ok = ok && mbar_wait(&sfree[s], h, 0x524);
-                if (ok) qk(h == 0 ? tile : tile + step, h ^ 1);
+                ok = ok && a5_wait(b_f, h, 0x524);
+                qk(h == 0 ? tile : tile + step, h ^ 1);
               }
-              if (h == 0) ok = ok && mbar_wait(&vfull[st], (tile >> 1) & 1, 0x526);
-              ok = ok && mbar_wait(&pfull[2 * s + h], turn, 0x527);
-              ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
+              if (h == 0) ok = ok && a5_wait(b_v + st * 8, (tile >> 1) & 1, 0x526);
+              ok = ok && a5_wait(b_p + h * 8, turn, 0x527);
               t5_fence_after();
+              __syncwarp();
               const uint64_t va = dv + st * kStep + ((h * 64 * 128) >> 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 a5_mma_ts(lead, tmo, tmp + h * 32 + k * 8, va + ((k * 2048) >> 4), id_o, (j > 0 || h > 0 || k > 0) ? 1u : 0u);
               a5_commit(lead, &pvdone[2 * s + h]);
             }
-            if (!ok) break;
             turn ^= 1;
             a5_commit(lead, &vempty[st]);
             if (!two) a5_commit(lead, &vempty[st]);
@@ -448,6 +468,8 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
       const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t ts = tl + s * 64, tp = tl + 128 + s * 64, to = tl + 256 + s * D;
       const int tok = tr / p.group, head = tr - tok * p.group;   // in the row tile
+      const uint32_t b_s = smem_u32(sfull + s), b_f = smem_u32(sfree + s), b_p = smem_u32(pfull + 2 * s),
+                     b_pv = smem_u32(pvdone + 2 * s);
       int jobs = 0;
       bool more = true, asked = false;               // asked: this item's q is on its way
       // (a stream without a tile of the item asks for nothing: the copy could land on the sums that go
@@ -482,13 +504,10 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         for (int q = 0; q < 2 * nj; ++q, ++jobs) {               // jobs: 64 keys of a tile
           const int h = q & 1;
           const int tile = two ? q >> 1 : 2 * (q >> 1) + s;
-          const int jt = w.base + tile;
-          const int slot = jt & (kA5ScaleSlots - 1);
-          if (ok && h == 0) ok = mbar_wait(&scfull[slot], (jt / kA5ScaleSlots) & 1, 0x529);
-          if (ok) ok = mbar_wait(&sfull[s], h, 0x52a);           // two jobs a tile: the parity is the half
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+          const int slot = (w.base + tile) & (kA5ScaleSlots - 1);
+          ok = ok && a5_wait(b_s, h, 0x52a);                     // two jobs a tile: the parity is the half
           t5_fence_after();
+          __syncwarp();
           float x[64];
           a5_ld32(ts, *reinterpret_cast<float(*)[32]>(&x[0]));
           a5_ld32(ts + 32, *reinterpret_cast<float(*)[32]>(&x[32]));
@@ -510,7 +529,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
           a5_wait32(*reinterpret_cast<float(*)[32]>(&x[32]));
           t5_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sfree[s]);
+          if (lane == 0) a5_arrive(b_f);
           // a warp whose rows all see all keys (nearly every one) tests none
           if (__any_sync(0xffffffffu, clo > 0 || chi < 64)) {
 #pragma unroll
@@ -536,9 +555,9 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
             m = nm;
             l *= al;
             if (q > 0) {
-              ok = __all_sync(0xffffffffu, mbar_wait(&pvdone[2 * s + (h ^ 1)], ((jobs - 1) >> 1) & 1, 0x52c));
-              if (!ok) break;
+              ok = ok && a5_wait(b_pv + (h ^ 1) * 8, ((jobs - 1) >> 1) & 1, 0x52c);
               t5_fence_after();
+              __syncwarp();
 #pragma unroll 1
               for (int c = 0; c < D; c += 32) {
                 float v[32];
@@ -579,12 +598,12 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
           a5_wait_st();
           t5_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&pfull[2 * s + h]);
+          if (lane == 0) a5_arrive(b_p + h * 8);
         }
         // the last two products of the item (the ones before are complete: their places hold the last S)
         if (ok && nj > 0) {
           const int ph = ((jobs - 1) >> 1) & 1;
-          ok = mbar_wait(&pvdone[2 * s], ph, 0x52b) && mbar_wait(&pvdone[2 * s + 1], ph, 0x52d);
+          ok = a5_wait(b_pv, ph, 0x52b) && a5_wait(b_pv + 8, ph, 0x52d);
         }
         ok = __all_sync(0xffffffffu, ok);
         t5_fence_after();
