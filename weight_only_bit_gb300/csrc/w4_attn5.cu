@@ -166,6 +166,11 @@ __device__ __forceinline__ bool a5_wait(uint32_t bar, uint32_t parity, uint32_t 
   atomicCAS(&g_error_word, 0u, site);
   return false;
 }
+__device__ __forceinline__ unsigned int a5_ld_acquire(const unsigned int* p) {
+  unsigned int v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 __device__ __forceinline__ void a5_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -600,6 +605,11 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
           __syncwarp();
           if (lane == 0) a5_arrive(b_p + h * 8);
         }
+        const bool whole = w.whole();
+        const int c0 = w.first_cta(sp), c1 = w.last_cta(sp);
+        unsigned int* ticket = reinterpret_cast<unsigned int*>(a.workspace) + c0;
+        unsigned int there = 0;                                  // pieces of the item that are written
+        if (!whole && tid == 0) there = a5_ld_acquire(ticket);
         // the last two products of the item (the ones before are complete: their places hold the last S)
         if (ok && nj > 0) {
           const int ph = ((jobs - 1) >> 1) & 1;
@@ -608,8 +618,14 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         ok = __all_sync(0xffffffffu, ok);
         t5_fence_after();
         // ---------------------------------------------------------------- the item's result
-        const bool whole = w.whole();
-        const int c0 = w.first_cta(sp), c1 = w.last_cta(sp);
+        // A piece that finds all others written keeps its own sums and joins: most items have two pieces, the
+        // second of them written long before the first, and 128 KB are neither written nor read again.
+        bool last = false;
+        if (!whole) {
+          if (tid == 0) *flag = there == (unsigned)(c1 - c0);
+          a5_sync_softmax();
+          last = *flag != 0;
+        }
         float* slots = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.workspace) + kAttnMaxCtas * 4);
         constexpr size_t SLOT = attn_slot_floats(kA5R, D);
         const int off = two ? s * 128 : 0;
@@ -673,22 +689,26 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
             a.lse[(long long)(it.start + qi) * a.q_heads + orow] =
                 ll > 0.f || ll != ll ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
         };
-        if (mine) {
+        // 32 channels of this row's own sums
+        auto own = [&](int c, float (&v)[32]) {
+          a5_get32(to + c, v);
+          if (!two) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(xo + ((size_t)((c + i) / 4) * 128 + tr) * 4);
+              v[i] = fmaf(y.x, f1, v[i] * f0);
+              v[i + 1] = fmaf(y.y, f1, v[i + 1] * f0);
+              v[i + 2] = fmaf(y.z, f1, v[i + 2] * f0);
+              v[i + 3] = fmaf(y.w, f1, v[i + 3] * f0);
+            }
+          }
+        };
+        if (mine && !last) {
           const float inv = l > 0.f || l != l ? __fdiv_rn(1.f, l) : 0.f;
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float v[32];
-            a5_get32(to + c, v);
-            if (!two) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 y = *reinterpret_cast<const float4*>(xo + ((size_t)((c + i) / 4) * 128 + tr) * 4);
-                v[i] = fmaf(y.x, f1, v[i] * f0);
-                v[i + 1] = fmaf(y.y, f1, v[i + 1] * f0);
-                v[i + 2] = fmaf(y.z, f1, v[i + 2] * f0);
-                v[i + 3] = fmaf(y.w, f1, v[i + 3] * f0);
-              }
-            }
+            own(c, v);
             if (whole) {
               put(c, v, inv);
             } else {
@@ -706,19 +726,23 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         }
         if (!whole) {
           // -------------------------------------------------------------- the last piece joins all of them
-          unsigned int* ticket = reinterpret_cast<unsigned int*>(a.workspace) + c0;
-          __threadfence();
-          a5_sync_softmax();
-          if (tid == 0) *flag = atomicAdd(ticket, 1u) == (unsigned)(c1 - c0);
-          a5_sync_softmax();
-          if (*flag && mine) {
+          if (!last) {
             __threadfence();
+            a5_sync_softmax();
+            if (tid == 0) *flag = atomicAdd(ticket, 1u) == (unsigned)(c1 - c0);
+            a5_sync_softmax();
+            last = *flag != 0;
+          }
+          if (last && mine) {
+            __threadfence();
+            // in key order, this piece's from its own sums: the result is the same whichever is last
             auto piece = [&](int c) { return slots + SLOT * (2 * c + (c == c0 ? 1 : 0)) + off + tr; };
+            auto top = [&](int c) { return c == cta ? m : __ldcg(piece(c) + (size_t)kA5R * D); };
             float mm = -INFINITY, ll = 0.f;
-            for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, __ldcg(piece(c) + (size_t)kA5R * D));
+            for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, top(c));
             const float b = mm == -INFINITY ? 0.f : mm;
             for (int c = c0; c <= c1; ++c)
-              ll = fmaf(__ldcg(piece(c) + (size_t)kA5R * (D + 1)), attn_ex2(__ldcg(piece(c) + (size_t)kA5R * D) - b), ll);
+              ll = fmaf(c == cta ? l : __ldcg(piece(c) + (size_t)kA5R * (D + 1)), attn_ex2(top(c) - b), ll);
             const float iv = ll > 0.f || ll != ll ? __fdiv_rn(1.f, ll) : 0.f;
 #pragma unroll 1
             for (int ch = 0; ch < D; ch += 32) {
@@ -727,11 +751,15 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
               for (int i = 0; i < 32; ++i) v[i] = 0.f;
 #pragma unroll 1
               for (int c = c0; c <= c1; ++c) {
-                const float* x = piece(c);
                 float y[32];
+                if (c == cta) {
+                  own(ch, y);
+                } else {
+                  const float* x = piece(c);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) y[i] = __ldcg(x + (size_t)(ch + i) * kA5R);
-                const float f = attn_ex2(__ldcg(x + (size_t)kA5R * D) - b);
+                  for (int i = 0; i < 32; ++i) y[i] = __ldcg(x + (size_t)(ch + i) * kA5R);
+                }
+                const float f = attn_ex2(top(c) - b);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = fmaf(y[i], f, v[i]);
               }
@@ -739,7 +767,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
             }
             if (valid) put_lse(mm, ll);
           }
-          if (*flag && tid == 0) *ticket = 0;
+          if (last && tid == 0) *ticket = 0;
         }
         if (!ok && lane == 0) *reinterpret_cast<volatile int*>(bad) = 1;
         a5_sync_softmax();                                       // Q's places and the flag are free again
