@@ -398,29 +398,28 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         constexpr uint32_t id_s = a5_idesc(64, false), id_o = a5_idesc(D, true);
         const uint32_t lead = a5_elect();
         constexpr uint64_t kStep = S::kTile >> 4;    // from a stage, or a stream's q, to the next
+        constexpr uint64_t kHalf = (64 * 128) >> 4;  // from half a tile to the other
         const uint64_t dq = a5_desc_k(sb + S::oQ) + s * kStep, dk = a5_desc_k(sb + S::oK), dv = a5_desc_mn(sb + S::oV);
         const uint32_t tms = tmem + s * 64, tmp = tmem + 128 + s * 64, tmo = tmem + 256 + s * D;
         const uint32_t b_q = smem_u32(qfull + s), b_k = smem_u32(kfull), b_v = smem_u32(vfull), b_s = smem_u32(sfull + s),
                        b_f = smem_u32(sfree + s), b_p = smem_u32(pfull + 2 * s);
-        uint32_t items = 0, turn = 0;                // parities of qfull and, by tile, of pfull
+        // parities of qfull, of sfree and, by place, of pfull
+        uint32_t items = 0, frees = 0, turn[2] = {0, 0};
         bool more = true;
         // (after a lost wait the walk goes on without waiting: the other warps' counts stay right)
         while (more) {
-          const int n = w.u1 - w.u0;
           const bool two = w.it.n - w.it.rb * tpb > p.tpt;
-          const int nj = two ? n : (n - s + 1) / 2;  // tiles of this stream: all, or every second
-          const int step = two ? 1 : 2;
-          if (nj > 0) {
-            ok = ok && a5_wait(b_q, items, 0x523);
-            items ^= 1;
-          }
-          // S of half h of a tile; the tile's keys are free after the second
+          const int h0 = two ? 0 : s;                // this stream's halves of a tile: both, or one
+          const int last = w.base + w.u1 - w.u0 - 1;
+          ok = ok && a5_wait(b_q, items, 0x523);
+          items ^= 1;
+          // S of half h of a tile; the tile's keys are free after the stream's last half
           auto qk = [&](int tile, int h) {
             const uint32_t st = tile & 1;
-            if (h == 0) ok = ok && a5_wait(b_k + st * 8, (tile >> 1) & 1, 0x525);
+            if (h == h0) ok = ok && a5_wait(b_k + st * 8, (tile >> 1) & 1, 0x525);
             t5_fence_after();
             __syncwarp();
-            const uint64_t ka = dk + st * kStep + ((h * 64 * 128) >> 4);
+            const uint64_t ka = dk + st * kStep + h * kHalf;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint64_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
@@ -428,35 +427,44 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
             }
             a5_commit(lead, &sfull[s]);
             if (lane == 0) a5_arrive(b_s);
-            if (h == 1) {
-              a5_commit(lead, &kempty[st]);
-              if (!two) a5_commit(lead, &kempty[st]);
-            }
+            if (h > h0 || !two) a5_commit(lead, &kempty[st]);
           };
-          int tile = w.base + (two ? 0 : s);
-          if (nj > 0) qk(tile, 0);                   // (the last S before was read: its P came)
-          for (int j = 0; j < nj; ++j, tile += step) {
+          // PV of half h of a tile, P in place pl
+          auto pv = [&](int tile, int h, int pl, uint32_t parity) {
             const uint32_t st = tile & 1;
+            if (h == h0) ok = ok && a5_wait(b_v + st * 8, (tile >> 1) & 1, 0x526);
+            ok = ok && a5_wait(b_p + pl * 8, parity, 0x527);
+            t5_fence_after();
+            __syncwarp();
+            const uint64_t va = dv + st * kStep + h * kHalf;
+            const uint32_t on = tile > w.base || h > h0 ? 1u : 0u;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              // the next S, once this one is in registers (a tile has two jobs: the parity is the half)
-              if (h == 0 || j + 1 < nj) {
-                ok = ok && a5_wait(b_f, h, 0x524);
-                qk(h == 0 ? tile : tile + step, h ^ 1);
-              }
-              if (h == 0) ok = ok && a5_wait(b_v + st * 8, (tile >> 1) & 1, 0x526);
-              ok = ok && a5_wait(b_p + h * 8, turn, 0x527);
-              t5_fence_after();
-              __syncwarp();
-              const uint64_t va = dv + st * kStep + ((h * 64 * 128) >> 4);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                a5_mma_ts(lead, tmo, tmp + h * 32 + k * 8, va + ((k * 2048) >> 4), id_o, (j > 0 || h > 0 || k > 0) ? 1u : 0u);
-              a5_commit(lead, &pvdone[2 * s + h]);
+            for (int k = 0; k < 4; ++k)
+              a5_mma_ts(lead, tmo, tmp + pl * 32 + k * 8, va + ((k * 2048) >> 4), id_o, k > 0 ? 1u : on);
+            a5_commit(lead, &pvdone[2 * s + pl]);
+            if (h > h0 || !two) a5_commit(lead, &vempty[st]);
+          };
+          qk(w.base, h0);                            // (the last S before was read: its P came)
+          if (two) {
+            for (int tile = w.base; tile <= last; ++tile) {
+              // the next S, once this one is in registers
+              ok = ok && a5_wait(b_f, frees, 0x524);
+              qk(tile, 1);
+              pv(tile, 0, 0, turn[0]);
+              ok = ok && a5_wait(b_f, frees ^ 1, 0x524);
+              if (tile < last) qk(tile + 1, 0);
+              pv(tile, 1, 1, turn[1]);
+              turn[0] ^= 1;
+              turn[1] ^= 1;
             }
-            turn ^= 1;
-            a5_commit(lead, &vempty[st]);
-            if (!two) a5_commit(lead, &vempty[st]);
+          } else {
+            for (int tile = w.base; tile <= last; ++tile) {
+              ok = ok && a5_wait(b_f, frees, 0x524);
+              frees ^= 1;
+              if (tile < last) qk(tile + 1, s);
+              if (tile & 1) pv(tile, s, 1, turn[1]); else pv(tile, s, 0, turn[0]);
+              if (tile & 1) turn[1] ^= 1; else turn[0] ^= 1;
+            }
           }
           more = w.next(a, tpb);
         }
@@ -475,14 +483,13 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
       const int tok = tr / p.group, head = tr - tok * p.group;   // in the row tile
       const uint32_t b_s = smem_u32(sfull + s), b_f = smem_u32(sfree + s), b_p = smem_u32(pfull + 2 * s),
                      b_pv = smem_u32(pvdone + 2 * s);
-      int jobs = 0;
+      uint32_t jobs = 0;                             // parity of sfull
+      uint32_t turn[2] = {1, 1};                     // parities of the places' last products (none yet: complete)
       bool more = true, asked = false;               // asked: this item's q is on its way
-      // (a stream without a tile of the item asks for nothing: the copy could land on the sums that go
-      // through q's places at the end)
       auto ask_q = [&](const Walk<kA5T, kA5Ov>& y) {
         const Item& x = y.it;
         const bool both = x.n - x.rb * tpb > p.tpt;
-        if (tr == 0 && (both || y.u1 - y.u0 > s)) {
+        if (tr == 0) {
           a5_fence_proxy();                                      // the places may have held sums of an item
           mbar_arrive_expect_tx(&qfull[s], (uint32_t)(p.tpt * p.group * D * 2));
           const int t0 = x.start + x.rb * tpb + (both ? s * p.tpt : 0);
@@ -505,18 +512,19 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         const int rhi = !valid ? 0x7fffffff : pos < 0 ? 0 : a.causal ? min(it.total, pos + 1) : it.total;
         const int rlo = !valid ? 0 : a.window > 0 ? pos - a.window + 1 : 0;
         float m = -INFINITY, l = 0.f;
-        const int nj = two ? n : (n - s + 1) / 2;
-        for (int q = 0; q < 2 * nj; ++q, ++jobs) {               // jobs: 64 keys of a tile
-          const int h = q & 1;
-          const int tile = two ? q >> 1 : 2 * (q >> 1) + s;
+        const int h0 = two ? 0 : s;                              // this stream's halves of a tile: both, or one
+        for (int q = h0; q < 2 * n; q += two ? 1 : 2) {          // jobs: 64 keys of a tile
+          const int h = q & 1, tile = q >> 1;
           const int slot = (w.base + tile) & (kA5ScaleSlots - 1);
-          ok = ok && a5_wait(b_s, h, 0x52a);                     // two jobs a tile: the parity is the half
+          const int pl = two ? h : (w.base + tile) & 1;          // place of P: every second job the same
+          ok = ok && a5_wait(b_s, jobs, 0x52a);
+          jobs ^= 1;
           t5_fence_after();
           __syncwarp();
           float x[64];
           a5_ld32(ts, *reinterpret_cast<float(*)[32]>(&x[0]));
           a5_ld32(ts + 32, *reinterpret_cast<float(*)[32]>(&x[32]));
-          if (two && q == 2 * nj - 1) {
+          if (two && q == 2 * n - 1) {
             // the item's products with q are complete: the next item's rows may come in
             Walk<kA5T, kA5Ov> nx = w;
             if (nx.next(a, tpb)) {
@@ -559,8 +567,8 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
             const float al = nm == m ? 1.f : attn_ex2(m - nm);   // 0 where there was nothing
             m = nm;
             l *= al;
-            if (q > 0) {
-              ok = ok && a5_wait(b_pv + (h ^ 1) * 8, ((jobs - 1) >> 1) & 1, 0x52c);
+            if (q > h0) {
+              ok = ok && a5_wait(b_pv + (pl ^ 1) * 8, pl ? turn[0] : turn[1], 0x52c);
               t5_fence_after();
               __syncwarp();
 #pragma unroll 1
@@ -598,12 +606,13 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
               l = fmaf(sum.x + sum.y, f.z, l);
             }
             // (the place is free: the P before the last was taken in ahead of this job's S)
-            a5_st16(tp + h * 32 + c * 16, pk);
+            a5_st16(tp + pl * 32 + c * 16, pk);
           }
           a5_wait_st();
           t5_fence_before();
           __syncwarp();
-          if (lane == 0) a5_arrive(b_p + h * 8);
+          if (lane == 0) a5_arrive(b_p + pl * 8);
+          if (pl) turn[1] ^= 1; else turn[0] ^= 1;
         }
         const bool whole = w.whole();
         const int c0 = w.first_cta(sp), c1 = w.last_cta(sp);
@@ -611,10 +620,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         unsigned int there = 0;                                  // pieces of the item that are written
         if (!whole && tid == 0) there = a5_ld_acquire(ticket);
         // the last two products of the item (the ones before are complete: their places hold the last S)
-        if (ok && nj > 0) {
-          const int ph = ((jobs - 1) >> 1) & 1;
-          ok = a5_wait(b_pv, ph, 0x52b) && a5_wait(b_pv + 8, ph, 0x52d);
-        }
+        ok = ok && a5_wait(b_pv, turn[0], 0x52b) && a5_wait(b_pv + 8, turn[1], 0x52d);
         ok = __all_sync(0xffffffffu, ok);
         t5_fence_after();
         // ---------------------------------------------------------------- the item's result
@@ -641,12 +647,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               float v[32];
-              if (nj > 0) {
-                a5_get32(to + c, v);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0.f;
-              }
+              a5_get32(to + c, v);
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
                 *reinterpret_cast<float4*>(xo + ((size_t)((c + i) / 4) * 128 + tr) * 4) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
