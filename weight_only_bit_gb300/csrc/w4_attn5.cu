@@ -45,8 +45,8 @@ constexpr int kA5R = 256;                    // rows per item, at most
 constexpr int kA5Ov = 2;                     // what an item costs beside its tiles
 constexpr int kA5Mma = 12;                   // the issuing warps: 12 and 13
 constexpr int kA5Threads = 512;
-// Registers a thread: launched with 128 each (65536 in all); 2 x 128 x 152 + 128 x 128 + 128 x 80 = 65536.
-constexpr int kA5RegsSoftmax = 152, kA5RegsMma = 80;
+// Registers a thread: launched with 128 each (65536 in all); 2 x 128 x 136 + 128 x 128 + 128 x 112 = 65536.
+constexpr int kA5RegsSoftmax = 136, kA5RegsMma = 112;
 constexpr float kA5Slack = 6.f;
 constexpr int kA5ScaleSlots = 4;
 
@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
             uint32_t pk[16];
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-              const float4 f = sc[2 * c + g];
+              const float4 f = a5_lds_f4(ssc + (2 * c + g) * 16);
               const float2 kk = make_float2(f.x, f.x), bb = make_float2(f.y - base, f.y - base);
               float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
