@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
           if (pl) turn[1] ^= 1; else turn[0] ^= 1;
         }
         const bool whole = w.whole();
-        const int c0 = w.first_cta(sp), c1 = w.last_cta(sp);
+        const int c0 = whole ? cta : w.first_cta(sp), c1 = whole ? cta : w.last_cta(sp);
         unsigned int* ticket = reinterpret_cast<unsigned int*>(a.workspace) + c0;
         unsigned int there = 0;                                  // pieces of the item that are written
         if (!whole && tid == 0) there = a5_ld_acquire(ticket);
@@ -669,6 +669,11 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         // 32 channels of the warp's rows: through shared memory, so that a store covers 64 bytes of 8 rows
         // (16 bytes of 32 rows would be twice the sectors and four times the lines).  By the whole warp.
         const uint32_t stage = sb + S::oOut + warp * 2048;
+        __half* rows[4];                                         // of the rows that this lane stores 16 bytes of
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          rows[k] = reinterpret_cast<__half*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(valid ? dst : nullptr), k * 8 + (lane >> 2)));
         auto put = [&](int c, const float (&v)[32], float scale) {
           __syncwarp();
 #pragma unroll
@@ -681,8 +686,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
           for (int k = 0; k < 4; ++k) {
             const int r = k * 8 + (lane >> 2);
             const float4 x = a5_lds_f4(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
-            __half* d = reinterpret_cast<__half*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(valid ? dst : nullptr), r));
-            if (d) *reinterpret_cast<float4*>(d + c + 8 * (lane & 3)) = x;
+            if (rows[k]) *reinterpret_cast<float4*>(rows[k] + c + 8 * (lane & 3)) = x;
           }
         };
         auto put_lse = [&](float mm, float ll) {
