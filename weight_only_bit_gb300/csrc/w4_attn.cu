@@ -46,7 +46,7 @@ constexpr int kAtMaxCtas = 160;              // CTAs of a launch, at most (piece
 template <int D, int NT>
 struct AtSmem {
   static constexpr int kStage = kAtT * D * 2;            // K, then V
-  static constexpr int kStages = NT <= 2 ? 3 : 2;        // per warp
+  static constexpr int kStages = 2;                      // per warp
   static constexpr int kRows = 8 * NT;
   static constexpr int kRing = kAtWarps * kStages * kStage;
   // one place for the split's prefix sums, then half of the warps' sums, and the pieces' (maximum, sum)
@@ -299,8 +299,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
       bool up = false;
       float mx[NT][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY;
-#pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int src = (i & 15) * 2 + x;
         const float ks = __shfl_sync(0xffffffffu, cur.ks, src), lvs = __shfl_sync(0xffffffffu, cur.lvs, src);
@@ -308,17 +306,27 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float v = fmaf(s[n][x][e], ks, lvs);
-            if (masked) {
-              const int key = k0 + x * 16 + (e >> 1) * 8 + pg;
-              v = key >= rlo[n][e & 1] && key < rhi[n][e & 1] ? v : -INFINITY;
-            }
-            s[n][x][e] = v;
-            mx[n][e & 1] = fmaxf(mx[n][e & 1], v);   // a NaN is left out here and comes back as a weight
-          }
+          for (int e = 0; e < 4; ++e) s[n][x][e] = fmaf(s[n][x][e], ks, lvs);
         }
       }
+      // (one branch for the whole tile here and one for V's below: a test at each value broke the tile's code
+      // into pieces that could not overlap)
+      if (masked) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = k0 + x * 16 + (e >> 1) * 8 + pg;
+              s[n][x][e] = key >= rlo[n][e & 1] && key < rhi[n][e & 1] ? s[n][x][e] : -INFINITY;
+            }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)                  // a NaN is left out here and comes back as a weight
+          mx[n][e] = fmaxf(fmaxf(s[n][0][e], s[n][0][2 + e]), fmaxf(s[n][1][e], s[n][1][2 + e]));
 #pragma unroll
       for (int n = 0; n < NT; ++n) up |= mx[n][0] > m[n][0] + kAtSlack || mx[n][1] > m[n][1] + kAtSlack;
       if (__any_sync(0xffffffffu, up)) {
@@ -369,12 +377,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
             const uint2 z = at_lds64(sv + at_swz<D>(rows[y], g >> 1) + (g & 1) * 8);
             v[y][0] = z.x; v[y][1] = z.y;
           }
-          // what lies outside [lo, hi) was never written here, or belongs to nobody: weight 0 times
-          // such a code must be 0, so the code is
-          if (masked && (k0 + rows[y] >= it.hi || k0 + rows[y] < it.lo)) {
+        }
+        // what lies outside [lo, hi) was never written here, or belongs to nobody: weight 0 times such a
+        // code must be 0, so the code is
+        if (masked) {
 #pragma unroll
-            for (int z = 0; z < NW; ++z) v[y][z] = 0u;
-          }
+          for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int z = 0; z < NW; ++z) v[y][z] = k0 + rows[y] >= it.hi || k0 + rows[y] < it.lo ? 0u : v[y][z];
         }
         // A rows g, g + 8 of channel tile c: channels 2c, 2c + 1 of the lane's D / 8
 #pragma unroll
