@@ -57,7 +57,9 @@ struct AtSmem {
   static constexpr int oMerge = kRing;
   static constexpr int oM = oMerge + kMerge;             // [warps][rows] maxima
   static constexpr int oL = oM + kAtWarps * kRows * 4;   // [warps][rows] sums
-  static constexpr int oBar = oL + kAtWarps * kRows * 4;
+  static constexpr bool kSharedQ = NT > 2;               // B fragments of q: [tile][step][lane] of 8 bytes
+  static constexpr int oQ = oL + kAtWarps * kRows * 4;
+  static constexpr int oBar = oQ + (kSharedQ ? NT * (D / 16) * 256 : 0);
   static constexpr int oFlag = oBar + kAtWarps * kStages * 8;
   static constexpr int kTotal = oFlag + 16 + 1024;       // and the alignment slack
 };
@@ -104,6 +106,10 @@ __device__ __forceinline__ uint2 at_lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
+}
+
+__device__ __forceinline__ void at_sts64(uint32_t a, uint2 v) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(a), "r"(v.x), "r"(v.y) : "memory");
 }
 
 // Byte offset of 16-byte chunk `c` of row `r` in a TMA-swizzled tile of D-byte rows.
@@ -209,32 +215,39 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
   const int f0 = t + 4 * (t & 1), f1 = f0 ^ 4;       // keys of an 8-key group that weights 2t, 2t + 1 belong to
   // the key of A row g (and g + 8): perm = {0, 4, 5, 1, 2, 6, 7, 3}
   const int pg = (g & 1) ? ((g >> 1) + 4 * ((g >> 1) & 1)) ^ 4 : (g >> 1) + 4 * ((g >> 1) & 1);
-  // B column g of each tile is a row of q
-  uint32_t qf[NT][D / 16][2];
+  // B column g of each tile is a row of q: up to two tiles in registers, more in shared memory (they would
+  // spill: three tiles of 128 channels and their accumulators are 144 registers)
+  constexpr bool kSharedQ = S::kSharedQ;
+  constexpr int NF = NT * (D / 16);          // fragments; and how many of them a lane loads
+  constexpr int NQ = kSharedQ ? (NF + kAtWarps - 1) / kAtWarps : NF;
+  uint2 qf[NQ];
   auto load_q = [&](const Item& x) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int row = n * 8 + g;
-      const bool valid = row < x.n * p.group;
-      const int tok = row / p.group;
+    for (int k = 0; k < NQ; ++k) {
+      const int f = kSharedQ ? k * kAtWarps + warp : k;
+      const int n = f / (D / 16), s = f % (D / 16), row = n * 8 + g, tok = row / p.group;
       const __half* q = a.q + (long long)(x.start + tok) * a.q_stride + (long long)(x.h * p.group + row - tok * p.group) * D;
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        uint2 v = make_uint2(0, 0);
-        if (valid) v = __ldg(reinterpret_cast<const uint2*>(q + 16 * (t + 4 * (s >> 2)) + 4 * (s & 3)));
-        qf[n][s][0] = v.x;
-        qf[n][s][1] = v.y;
-      }
+      qf[k] = make_uint2(0, 0);
+      if (f < NF && row < x.n * p.group) qf[k] = __ldg(reinterpret_cast<const uint2*>(q + 16 * (t + 4 * (s >> 2)) + 4 * (s & 3)));
     }
   };
-  // (more row tiles leave no registers for the next item's)
-  constexpr bool kEarly = NT <= 2;
-  if (kEarly) load_q(w.it);
+  const uint32_t sq = smem_u32(smem) + S::oQ + lane * 8;
+  auto share_q = [&] {                               // all warps are past the item before
+    if (kSharedQ) {
+#pragma unroll
+      for (int k = 0; k < NQ; ++k)
+        if (k * kAtWarps + warp < NF) at_sts64(sq + (k * kAtWarps + warp) * 256, qf[k]);
+    }
+  };
+  load_q(w.it);
+  if (kSharedQ) {
+    share_q();
+    __syncthreads();
+  }
   int i = 0;                                         // this warp's units so far
   bool ok = true, more = true;
   while (more) {
     const Item& it = w.it;
-    if (!kEarly) load_q(it);
     const int shift = it.total - it.n;
     // columns 2t and 2t + 1 of each tile: the keys [rlo, rhi) that they see
     int rlo[NT][2], rhi[NT][2];
@@ -274,25 +287,59 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
       const bool masked = k0 < full_lo || k0 + kAtT > full_hi;
       float s[NT][2][4];                             // [tile][16 keys][A rows g, g + 8 x B columns 2t, 2t + 1]
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[n][x][e] = 0.f;
+      // q from registers: 16 keys after the other; from shared memory: both with each fragment
+      auto words = [&](int x, int hf, uint32_t (&wk)[2][4]) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint4 z = at_lds128(sk + at_swz<D>(x * 16 + r * 8 + pg, t + 4 * hf));
+          wk[r][0] = z.x; wk[r][1] = z.y; wk[r][2] = z.z; wk[r][3] = z.w;
+        }
+      };
+      if constexpr (kSharedQ) {
 #pragma unroll
         for (int hf = 0; hf < D / 64; ++hf) {
-          const uint4 ka = at_lds128(sk + at_swz<D>(x * 16 + pg, t + 4 * hf));
-          const uint4 kb = at_lds128(sk + at_swz<D>(x * 16 + 8 + pg, t + 4 * hf));
-          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+          uint32_t wk[2][2][4];
+          words(0, hf, wk[0]);
+          words(1, hf, wk[1]);
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            uint32_t a0, a1, a2, a3;
-            at_cvt4(wa[y], a0, a2);
-            at_cvt4(wb[y], a1, a3);
+            uint2 b[NT];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) at_mma(s[n][x], a0, a1, a2, a3, qf[n][hf * 4 + y][0], qf[n][hf * 4 + y][1]);
+            for (int n = 0; n < NT; ++n) b[n] = at_lds64(sq + (n * (D / 16) + hf * 4 + y) * 256);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint32_t a0, a1, a2, a3;
+              at_cvt4(wk[x][0][y], a0, a2);
+              at_cvt4(wk[x][1][y], a1, a3);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) at_mma(s[n][x], a0, a1, a2, a3, b[n].x, b[n].y);
+            }
           }
         }
+      } else {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int hf = 0; hf < D / 64; ++hf) {
+            uint32_t wk[2][4];
+            words(x, hf, wk);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              uint32_t a0, a1, a2, a3;
+              at_cvt4(wk[0][y], a0, a2);
+              at_cvt4(wk[1][y], a1, a3);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                const uint2 b = qf[n * (D / 16) + hf * 4 + y];
+                at_mma(s[n][x], a0, a1, a2, a3, b.x, b.y);
+              }
+            }
+          }
       }
       // logits; the two groups' scales come from the lanes that know them
       float ivs[2];
@@ -408,7 +455,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
     // the next item's rows of q, on their way during the join
     Walk<kAtT, kAtOv> after = w;
     more = after.next(a, a.max_q);
-    if (kEarly && more) load_q(after.it);
+    if (more) load_q(after.it);
     // ---------------------------------------------------------------- join the warps
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -419,6 +466,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
         if (g == 0) sm[warp * R + n * 8 + 2 * t + e] = m[n][e];
       }
     __syncthreads();                                 // maxima in; the buffers of the last item are free
+    share_q();
     // lane (g, t) holds rows 2t, 2t + 1 of each tile, channels NCH g ... : accumulators over the warps'
     // common maximum, the upper warps' through shared memory onto the lower ones'
     constexpr int NCH = D / 8;
@@ -467,7 +515,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
     }
     __syncthreads();
     const bool whole = w.whole();
-    const int c0 = w.first_cta(sp), c1 = w.last_cta(sp);
     float* slots = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.workspace) + kAttnMaxCtas * 4);
     constexpr size_t SLOT = attn_slot_floats(R, D);
     float* part = slots + SLOT * (2 * cta + (w.u0 == 0 ? 1 : 0));
@@ -482,8 +529,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
       if (a.lse && ch == 0)
         a.lse[(long long)(it.start + r) * a.q_heads + head] = some ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
     };
-    for (int e = tid; e < R * (D / 4); e += kAtThreads) {
-      const int row = e / (D / 4), ch = e % (D / 4);
+    // four channels of NE rows a thread
+    constexpr int NE = (R * (D / 4) + kAtThreads - 1) / kAtThreads;
+    auto row_of = [&](int j) { return (tid + j * kAtThreads) / (D / 4); };
+    const int ch = tid % (D / 4);
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      const int row = row_of(j);
+      if (row >= R) continue;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       float ll = 0.f, mm = -INFINITY;
 #pragma unroll
@@ -511,6 +564,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
     }
     if (!whole) {
       // ------------------------------------------------------------ the last piece joins all of them
+      const int c0 = w.first_cta(sp), c1 = w.last_cta(sp);
       unsigned int* ticket = reinterpret_cast<unsigned int*>(a.workspace) + c0;
       __threadfence();
       __syncthreads();
@@ -518,11 +572,26 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
       __syncthreads();
       if (*flag) {
         __threadfence();
-        // maxima and sums of all pieces at once, a warp per row for the common maximum and the weights,
-        // then 16 pieces' sums in flight per thread
+        // sums, maxima and sums of weights of the first pieces at once, then a warp per row for the common
+        // maximum and the factors
         const int np = c1 - c0 + 1;
+        constexpr int KB = NE == 1 ? 16 : (NE == 2 ? 4 : 2);       // pieces in flight
         float2* pml = reinterpret_cast<float2*>(merge);              // [piece][row]
         auto piece = [&](int k) { return slots + SLOT * (2 * (c0 + k) + (k == 0 ? 1 : 0)); };
+        const int rows = it.n * p.group;             // that there are
+        float4 y[KB][NE];
+        auto fetch = [&](int k0) {
+#pragma unroll
+          for (int k = 0; k < KB; ++k)
+#pragma unroll
+            for (int j = 0; j < NE; ++j)
+{
+              y[k][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (k0 + k < np && row_of(j) < rows)
+                y[k][j] = __ldcg(reinterpret_cast<const float4*>(piece(k0 + k) + (size_t)row_of(j) * D + 4 * ch));
+            }
+        };
+        fetch(0);
         for (int e = tid; e < np * R; e += kAtThreads) {
           const float* s = piece(e / R) + (size_t)R * D + e % R;
           pml[e] = make_float2(__ldcg(s), __ldcg(s + R));
@@ -548,28 +617,26 @@ __global__ void __launch_bounds__(kAtThreads, 1) w4_attn_kernel(const __grid_con
           }
         }
         __syncthreads();
-        for (int e = tid; e < R * (D / 4); e += kAtThreads) {
-          const int row = e / (D / 4), ch = e % (D / 4);
-          if (row >= it.n * p.group) continue;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int k0 = 0; k0 < np; k0 += 16) {
-            float4 y[16];
+        float4 z[NE];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (k0 + k < np) y[k] = __ldcg(reinterpret_cast<const float4*>(piece(k0 + k) + (size_t)row * D + 4 * ch));
-            }
+        for (int j = 0; j < NE; ++j) z[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < np; k0 += KB) {
+          if (k0 > 0) fetch(k0);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float f = k0 + k < np ? pml[(k0 + k) * R + row].x : 0.f;
-              v.x = fmaf(y[k].x, f, v.x);
-              v.y = fmaf(y[k].y, f, v.y);
-              v.z = fmaf(y[k].z, f, v.z);
-              v.w = fmaf(y[k].w, f, v.w);
+          for (int k = 0; k < KB; ++k) {
+#pragma unroll
+            for (int j = 0; j < NE; ++j) {
+              const float f = k0 + k < np ? pml[(k0 + k) * R + min(row_of(j), R - 1)].x : 0.f;
+              z[j].x = fmaf(y[k][j].x, f, z[j].x);
+              z[j].y = fmaf(y[k][j].y, f, z[j].y);
+              z[j].z = fmaf(y[k][j].z, f, z[j].z);
+              z[j].w = fmaf(y[k][j].w, f, z[j].w);
             }
           }
-          store(row, ch, v, sm[row], sl[row]);
         }
+#pragma unroll
+        for (int j = 0; j < NE; ++j)
+          if (row_of(j) < R) store(row_of(j), ch, z[j], sm[row_of(j)], sl[row_of(j)]);
         __syncthreads();                             // the next item's maxima go to the same places
         if (tid == 0) *ticket = 0;
       }

@@ -28,6 +28,12 @@ __device__ __forceinline__ float attn_ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ unsigned int ld_acquire_gpu(const unsigned int* p) {
+  unsigned int v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 struct Item {
   int b, h, rb;        // sequence, kv head, token block
   int start, n, total; // first row of the sequence, its rows, its tokens in the cache

@@ -166,11 +166,6 @@ __device__ __forceinline__ bool a5_wait(uint32_t bar, uint32_t parity, uint32_t 
   atomicCAS(&g_error_word, 0u, site);
   return false;
 }
-__device__ __forceinline__ unsigned int a5_ld_acquire(const unsigned int* p) {
-  unsigned int v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
 __device__ __forceinline__ void a5_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -618,7 +613,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         const int c0 = whole ? cta : w.first_cta(sp), c1 = whole ? cta : w.last_cta(sp);
         unsigned int* ticket = reinterpret_cast<unsigned int*>(a.workspace) + c0;
         unsigned int there = 0;                                  // pieces of the item that are written
-        if (!whole && tid == 0) there = a5_ld_acquire(ticket);
+        if (!whole && tid == 0) there = ld_acquire_gpu(ticket);
         // the last two products of the item (the ones before are complete: their places hold the last S)
         ok = ok && a5_wait(b_pv, turn[0], 0x52b) && a5_wait(b_pv + 8, turn[1], 0x52d);
         ok = __all_sync(0xffffffffu, ok);
