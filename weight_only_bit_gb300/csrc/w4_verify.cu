@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(kVfThreads) w4_verify_stats_kernel(const __gri
                                                                      int rows) {
   __shared__ float2 red[kVfThreads / 32];
   __shared__ unsigned long long redk[kVfThreads / 32];
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();                   // (after the wait: what the second launch reads of the inputs is there)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int piece = (int)blockIdx.x % pl.pieces;
   const int br = (int)blockIdx.x / pl.pieces;
@@ -361,7 +361,6 @@ __global__ void __launch_bounds__(kVfThreads) w4_verify_pick_kernel(const __grid
   __shared__ unsigned long long red[kVfThreads / 32];
   __shared__ int s_last;
   pdl_launch_dependents();
-  pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int part = (int)blockIdx.x % pl.parts;
   const int b = (int)blockIdx.x / pl.parts;
@@ -370,30 +369,41 @@ __global__ void __launch_bounds__(kVfThreads) w4_verify_pick_kernel(const __grid
   const float c = 1.4426950408889634f / (greedy ? 1.f : a.temperature);
   const int n = vf_count(a, b);
   const bool with_q = rows > a.drafts + 1;
+  // Beside the first launch's last CTAs: what does not depend on the statistics.  Lane i has drafted token i
+  // (W4_MAX_DRAFTS < 32), its logits, and the part's times come into L2.
+  int x = -1;
+  float xl = -INFINITY, ql = -INFINITY, xu = 0.f;
+  if (lane < n) {
+    x = __ldg(a.draft_tokens + (long long)b * a.drafts + lane);
+    if (x >= 0 && x < a.vocab) {
+      xl = vf_logit(vf_row(a, b, lane)[x]);
+      if (!greedy) xu = __ldg(a.u + (long long)b * a.drafts + lane);
+      if (with_q) ql = vf_logit(vf_row(a, b, a.drafts + 1 + lane)[x]);
+    }
+  }
+  if (!greedy) {
+    const int v1 = min((part + 1) * pl.part, a.vocab);
+    for (int v = part * pl.part + tid * 32; v < v1; v += kVfThreads * 32)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.e + (long long)b * a.vocab + v));
+  }
+  pdl_wait();
   for (int r = warp; r < rows; r += kVfThreads / 32) {
     if (r <= a.drafts ? r > n : r - a.drafts - 1 >= n) continue;
     const RowStat s = vf_row_stat(ws, b * rows + r, pl.pieces, greedy, lane);
     if (lane == 0) stat[r] = s;
   }
   __syncthreads();
-  // every warp decides for itself: lane i looks at drafted token i (W4_MAX_DRAFTS < 32)
+  // every warp decides for itself
   bool refuse = true;
-  int x = -1;
   float lp = 0.f;
-  if (lane < n) {
-    x = __ldg(a.draft_tokens + (long long)b * a.drafts + lane);
-    if (x >= 0 && x < a.vocab) {
-      const RowStat s = stat[lane];
-      const float logit = vf_logit(vf_row(a, b, lane)[x]);
-      lp = logit == -INFINITY ? -INFINITY : vf_log2p(logit, s, c) * 0.6931471805599453f;
-      if (greedy) {
-        refuse = !(s.at == x && s.m != -INFINITY);
-      } else {
-        const float p = vf_prob(logit, s, c);
-        const float u = __ldg(a.u + (long long)b * a.drafts + lane);
-        const float q = with_q ? vf_prob(vf_logit(vf_row(a, b, a.drafts + 1 + lane)[x]), stat[a.drafts + 1 + lane], c) : 1.f;
-        refuse = !(__fmul_rn(u, q) < p);
-      }
+  if (lane < n && x >= 0 && x < a.vocab) {
+    const RowStat s = stat[lane];
+    lp = xl == -INFINITY ? -INFINITY : vf_log2p(xl, s, c) * 0.6931471805599453f;
+    if (greedy) {
+      refuse = !(s.at == x && s.m != -INFINITY);
+    } else {
+      const float q = with_q ? vf_prob(ql, stat[a.drafts + 1 + lane], c) : 1.f;
+      refuse = !(__fmul_rn(xu, q) < vf_prob(xl, s, c));
     }
   }
   const int acc = __ffs(__ballot_sync(0xffffffffu, refuse)) - 1;   // lane n always refuses
