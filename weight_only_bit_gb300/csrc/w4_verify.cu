@@ -39,7 +39,7 @@ struct VerifyPlan {
 
 static VerifyPlan plan_verify(int batch, int rows, int vocab, int sms) {
   VerifyPlan p;
-  // about sixteen CTAs per SM (four run at once), at least 4096 tokens each (16 a thread)
+  // about sixteen CTAs per SM (four or five run at once), at least 4096 tokens each (16 a thread)
   const long long want = 16LL * sms;
   auto cut = [&](long long n, int most) {
     long long k = want / n;
@@ -180,9 +180,10 @@ __device__ __forceinline__ int vf_count(const VerifyArgs& a, int b) {
   return a.n_drafts ? min(max(__ldg(a.n_drafts + b), 0), a.drafts) : a.drafts;
 }
 
-// First launch: CTA = one piece of one row.
+// First launch: CTA = one piece of one row.  Five CTAs an SM: at four the loads in flight do not cover DRAM
+// (batch of 48: 50 us for the call, 48 at five, 57 at six, whose registers spill).
 template <bool GREEDY>
-__global__ void __launch_bounds__(kVfThreads) w4_verify_stats_kernel(const __grid_constant__ VerifyArgs a, VerifyPlan pl,
+__global__ void __launch_bounds__(kVfThreads, 5) w4_verify_stats_kernel(const __grid_constant__ VerifyArgs a, VerifyPlan pl,
                                                                      int rows) {
   __shared__ float2 red[kVfThreads / 32];
   __shared__ unsigned long long redk[kVfThreads / 32];
