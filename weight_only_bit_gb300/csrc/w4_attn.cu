@@ -22,8 +22,14 @@
 // weights turn by one 8 x 8 transpose per tile; V's codes of two keys are interleaved by byte permutes
 // into A pairs.  The keys of an 8-key group are permuted so that both loads are free of bank
 // conflicts under the swizzle (perm below).
-// What bounds it: the bytes of the cache at long contexts; launch, dependent loads of the page table
-// and the join at short ones.
+// Measured (GB300, D = 128, pages of 64 and 32): 131071 keys of one sequence on 2 kv heads 21.8 us, 3.1 TB/s;
+// 64 sequences of up to 8192 keys, 6 rows each: 29.4 us, 4.5 TB/s; 16 of up to 6001 keys, 20 rows: 37.8 us,
+// 2.8 TB/s; 257 keys: 6.8 us.
+// What bounds it: with one row tile the bytes of the cache while the units run (6.6 TB/s), but 6 us go
+// before the first data (split, page table, scales, each a trip to DRAM) and 4 to 8 us after the last
+// (join of the warps, then of the pieces).  With three row tiles the instructions of a unit: 1000 with
+// two warps on a scheduler, each waiting for the one before it; two row tiles' q is in registers, more
+// come from shared memory (in registers they spilled: 40.7 us for the drafts).
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -39,7 +45,9 @@ namespace w4 {
 constexpr int kAtT = 32;                     // keys per unit
 constexpr int kAtWarps = 8;
 constexpr int kAtThreads = kAtWarps * 32;
-constexpr int kAtOv = 32;                    // what an item costs beside its units
+// What an item costs beside its units, four for each warp: 64 sequences of up to 8192 tokens 38 us at 4, 31 at 32,
+// 34 at 64; drafts of 16 sequences 57, 42 and 50 us.
+constexpr int kAtOv = 32;
 constexpr float kAtSlack = 6.f;
 constexpr int kAtMaxCtas = 160;              // CTAs of a launch, at most (pieces of an item)
 

@@ -9,12 +9,14 @@
 //
 // A row tile is as many whole tokens (all query heads of the group) as fit 128 rows, one TMA box of q.
 // An item has up to two row tiles, each with its own S, O and softmax warpgroup ("streams").  An item
-// of one row tile gives both streams the same rows and every second key tile each, joined at the
-// end; so the two softmax warpgroups always overlap the other's products.
+// of one row tile gives both streams the same rows and half of each key tile each, joined at the end; so
+// the two softmax warpgroups always overlap the other's products.  (Every second key tile each left a
+// stream with one stage of keys: 229 us for a prompt of 8191 tokens, 223 with the halves.)
 // Work goes in jobs of 64 keys (half a key tile).  Tensor memory is full: S 2 x 64 columns, the weights P
 // 2 x 2 x 32 (FP16, the A operand of the second product; two places per stream), O 2 x D (256 at
 // D = 128).  P has places of its own, not those of S: as soon as a job's S is in registers, the next
-// one's product runs, beside the exponentials.
+// one's product runs, beside the exponentials.  (S of 128 columns with P over it halves the hand-overs
+// and reads q half as often from shared memory, but the next S has to wait: 229 us against 198.)
 // Roles (four warpgroups of 128 threads; registers move from the last to the first two), connected by
 // mbarriers:
 //   warps 0-3, 4-7   softmax of stream 0 and 1: a thread per row, one pass over its S, 64 keys at a time:
@@ -26,7 +28,14 @@
 //   warps 12, 13     issue the MMAs of stream 0 and 1: the next S, then PV (the whole warp walks,
 //                    one elected lane issues: descriptors stay in uniform registers).  One warp for both
 //                    streams spent as long on waits and commits as the products take.
-// What bounds it: figures beside the launch below.
+// Measured (GB300): a causal prompt of 8191 tokens, 12 heads on 2, D = 128: 198 us, 1040 TFLOP/s, 53 % of
+// the measured FP16 rate.  8 chunks of up to 517 tokens, window 4096, 16 heads on 4, D = 64: 76 us.
+// What bounds it: no unit alone.  A job pair (one of each stream) takes 2000 cycles: tensor pipe 1300
+// (S at 48 cycles an instruction of 64 keys, bound by shared memory reading q again each time; PV at 64),
+// maxima and exponentials of the two warps of a scheduler 1050, with hand-overs of 130 cycles each and
+// the loads of S between them.  Without exponentials the prompt takes 194 us, without the maxima 188,
+// without the products 163, without the loads of the cache 184.  Beginning and ending an item costs
+// 8000 cycles (kA5Ov), half of it the stores of 64 KB.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -42,10 +51,13 @@ namespace w4 {
 
 constexpr int kA5T = 128;                    // keys per tile
 constexpr int kA5R = 256;                    // rows per item, at most
-constexpr int kA5Ov = 2;                     // what an item costs beside its tiles
+// What an item costs beside its tiles (8191-token prompt, windowed chunks: 224, 82 us at 1; 198, 76 at 2; 200, 78 at
+// 3; 204, 78 at 6).
+constexpr int kA5Ov = 2;
 constexpr int kA5Mma = 12;                   // the issuing warps: 12 and 13
 constexpr int kA5Threads = 512;
-// Registers a thread: launched with 128 each (65536 in all); 2 x 128 x 136 + 128 x 128 + 128 x 112 = 65536.
+// Registers a thread, so that no role spills in its loop (the issuing warps at 80 did: 223 us for the prompt,
+// 198 now); launched with 128 each (65536 in all); 2 x 128 x 136 + 128 x 128 + 128 x 112 = 65536.
 constexpr int kA5RegsSoftmax = 136, kA5RegsMma = 112;
 constexpr float kA5Slack = 6.f;
 constexpr int kA5ScaleSlots = 4;
@@ -791,8 +803,14 @@ static cudaError_t launch_attn5_d(A5Params& p, cudaStream_t stream) {
   auto kern = w4_attn5_kernel<D>;
   static_assert(A5Smem<D>::kTotal <= 227 * 1024, "shared memory of one CTA");
   static FuncAttrCache attrs;
-  cudaError_t ea = attrs.ensure(
-      [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, A5Smem<D>::kTotal); });
+  cudaError_t ea = attrs.ensure([&] {
+    // the roles share out the registers that the launch gives: with fewer, an increase would wait for ever
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs * kA5Threads < 256 * kA5RegsSoftmax + 128 * 128 + 128 * kA5RegsMma) return cudaErrorLaunchOutOfResources;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, A5Smem<D>::kTotal);
+  });
   if (ea != cudaSuccess) return ea;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)device_sm_count());

@@ -14,6 +14,8 @@
 // 128 channels are 64 of them a thread) they cost more in occupancy than they saved (two prompts of
 // 8191 tokens, 32 + 2 x 8 heads: 86 us with all held at 152 registers, 72 with half at 96, 70 with
 // none at 80).  Rows of q need no such unit: a warp per row, four heads' loads in flight per lane.
+// Measured (GB300): the prompts 70 us, 5.4 TB/s, 79 % of the measured copy rate; 256 sequences of one token
+// 3.6 us, one sequence 2.9 us, a launch and two dependent trips to memory.
 // What bounds it: DRAM bytes for prompts (q read and written, k and v read, codes written), launch
 // latency for single tokens.
 #include <cstdint>
