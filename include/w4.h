@@ -374,7 +374,8 @@ int w4_attn_kv8(const w4_kv_cache* cache, const uint16_t* q, uint16_t* out, floa
  *             probability), then -1;  accepted  [batch]: how many were accepted
  *   logprob   [batch][drafts + 1] or NULL: ln p_i(token) (temperature 1 where temperature is 0), 0 after
  *             the new token
- * 1 <= drafts <= W4_MAX_DRAFTS, 1 <= vocab <= 2^24.  Pointers aligned to their element.  workspace as
+ * 1 <= drafts <= W4_MAX_DRAFTS, 1 <= vocab <= 2^24; a temperature between 0 and 1e-4 is
+ * W4_ERR_UNSUPPORTED.  Pointers aligned to their element.  workspace as
  * for w4_attn_kv8, w4_spec_verify_workspace_bytes(...) bytes. */
 #define W4_MAX_DRAFTS 31
 int64_t w4_spec_verify_workspace_bytes(int batch, int drafts, int vocab);
