@@ -335,6 +335,21 @@ int w4_kv_append(const w4_kv_cache* cache, const uint16_t* q, const uint16_t* k,
                  int rotary_dim, int interleaved, int64_t q_stride, int64_t k_stride, int64_t v_stride,
                  int64_t q_out_stride, w4_stream_t stream);
 
+/* The same call with its arguments in one block, read before it returns: for callers whose foreign-function
+ * interface pays for each argument (from Python, 22 of them take longer than the kernel for one token). */
+typedef struct {
+  const w4_kv_cache* cache;
+  const uint16_t *q, *k, *v;
+  uint16_t* q_out;
+  const float *rope_cos, *rope_sin;
+  const int32_t *positions, *q_start, *kv_len;
+  w4_stream_t stream;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  int tokens, batch, q_heads, max_q, max_position, rotary_dim, interleaved;
+  int reserved;               /* 0 */
+} w4_kv_append_args;
+int w4_kv_append_block(const w4_kv_append_args* args);
+
 /* w4_attn_kv8 -- attention of the new rows over the cache (their own tokens appended before).  Query
  * head h reads key/value head h / (q_heads / kv_heads).  A row at position p sees the keys j with
  * 0 <= j < kv_len, j <= p if `causal`, and j > p - window if window > 0:
@@ -354,6 +369,22 @@ int w4_attn_kv8(const w4_kv_cache* cache, const uint16_t* q, uint16_t* out, floa
                 const int32_t* kv_len, int tokens, int batch, int q_heads, int max_q, float softmax_scale, int causal,
                 int window, int64_t q_stride, int64_t out_stride, void* workspace, int64_t workspace_bytes,
                 w4_stream_t stream);
+
+/* The same call with its arguments in one block (as w4_kv_append_block). */
+typedef struct {
+  const w4_kv_cache* cache;
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  const int32_t *q_start, *kv_len;
+  void* workspace;
+  w4_stream_t stream;
+  int64_t q_stride, out_stride, workspace_bytes;
+  int tokens, batch, q_heads, max_q, causal, window;
+  float softmax_scale;
+  int reserved;               /* 0 */
+} w4_attn_kv8_args;
+int w4_attn_kv8_block(const w4_attn_kv8_args* args);
 
 /* w4_spec_verify -- verification of drafted tokens (speculative sampling) from logits and given
  * random numbers.  Sequence b has n = drafts tokens drafted (n = n_drafts[b], clamped to

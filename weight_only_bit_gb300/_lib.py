@@ -41,7 +41,8 @@ SYMBOLS = (
     "w4_step_launch", "w4_step_destroy", "w4_status_str", "w4_last_cuda_error", "w4_device_check",
     "w4_launch_count", "w4_inject_timeout_once", "w4_gemv_levels_noalloc", "w4_gemv_plan",
     "w4_quantize_fp4", "w4_dequantize_fp4", "w4_gemv_fp4", "w4_step_run_host",
-    "w4_kv_append", "w4_attn_workspace_bytes", "w4_attn_kv8", "w4_spec_verify_workspace_bytes", "w4_spec_verify",
+    "w4_kv_append", "w4_kv_append_block", "w4_attn_workspace_bytes", "w4_attn_kv8", "w4_attn_kv8_block", "w4_spec_verify_workspace_bytes",
+    "w4_spec_verify",
 )
 
 
@@ -131,8 +132,10 @@ def _declare(L):
         "w4_inject_timeout_once": (I, []),
         "w4_gemv_levels_noalloc": (I, [ctypes.POINTER(GemvDesc), I, P]),
         "w4_kv_append": (I, [C, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, L64, L64, L64, L64, P]),
+        "w4_kv_append_block": (I, [ctypes.c_char_p]),
         "w4_attn_workspace_bytes": (L64, [I, I, I, I, I]),
         "w4_attn_kv8": (I, [C, P, P, P, P, P, I, I, I, I, F, I, I, L64, L64, P, L64, P]),
+        "w4_attn_kv8_block": (I, [ctypes.c_char_p]),
         "w4_spec_verify_workspace_bytes": (L64, [I, I, I]),
         "w4_spec_verify": (I, [P, P, P, P, P, P, P, P, I, I, I, F, P, L64, L64, P, L64, P]),
         "w4_gemv_plan": (I, [I, I, I, I, I, I, ctypes.POINTER(GemvPlan)]),

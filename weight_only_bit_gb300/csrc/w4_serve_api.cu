@@ -99,6 +99,13 @@ int w4_kv_append(const w4_kv_cache* cache, const uint16_t* q, const uint16_t* k,
   return launched(w4::launch_kv_append(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+int w4_kv_append_block(const w4_kv_append_args* p) {
+  if (!p) return W4_ERR_NULL;
+  return w4_kv_append(p->cache, p->q, p->k, p->v, p->q_out, p->rope_cos, p->rope_sin, p->positions, p->q_start,
+                      p->kv_len, p->tokens, p->batch, p->q_heads, p->max_q, p->max_position, p->rotary_dim,
+                      p->interleaved, p->q_stride, p->k_stride, p->v_stride, p->q_out_stride, p->stream);
+}
+
 int64_t w4_attn_workspace_bytes(int tokens, int batch, int q_heads, int kv_heads, int head_dim) {
   if (tokens < 0 || batch < 1 || q_heads < 1 || kv_heads < 1 || (head_dim != 64 && head_dim != 128)) return 0;
   return w4::attn_workspace_bytes(tokens, batch, q_heads, kv_heads, head_dim);
@@ -134,6 +141,13 @@ int w4_attn_kv8(const w4_kv_cache* cache, const uint16_t* q, uint16_t* out, floa
   a.window = window;
   a.workspace = workspace;
   return launched(w4::launch_attn(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int w4_attn_kv8_block(const w4_attn_kv8_args* p) {
+  if (!p) return W4_ERR_NULL;
+  return w4_attn_kv8(p->cache, p->q, p->out, p->lse, p->q_start, p->kv_len, p->tokens, p->batch, p->q_heads, p->max_q,
+                     p->softmax_scale, p->causal, p->window, p->q_stride, p->out_stride, p->workspace,
+                     p->workspace_bytes, p->stream);
 }
 
 int64_t w4_spec_verify_workspace_bytes(int batch, int drafts, int vocab) {
