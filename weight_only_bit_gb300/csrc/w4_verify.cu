@@ -18,8 +18,8 @@
 // order of arrival does not matter.  Scores are compared by an approximate quotient first; only what
 // comes within its error of the best so far is divided exactly.
 // Measured (GB300, vocabulary 151936): 48 sequences of 5 drafts with their logits 48 us, 3.9 TB/s (the first
-// launch 4.9 TB/s, the race 2.5); one sequence of 4 drafts 10.7 us; 16 sequences of 7 drafts, 32003 tokens,
-// no draft logits 11.8 us.
+// launch 4.9 TB/s, the race 2.5); one sequence of 4 drafts 9.4 us; 16 sequences of 7 drafts, 32003 tokens,
+// no draft logits 10.1 us.
 // What bounds it: the instructions beside the DRAM bytes of the logits for a batch (a conversion and an
 // exponential per logit: half of the issue slots), launches and dependent loads for one sequence.
 #include <cstdint>
@@ -34,7 +34,7 @@ namespace w4 {
 
 constexpr int kVfThreads = 256;
 constexpr int kVfMaxPieces = 64;            // pieces of one row in the first launch
-constexpr int kVfMaxParts = 64;             // CTAs of one sequence in the second
+constexpr int kVfMaxParts = 96;             // CTAs of one sequence in the second
 
 struct VerifyPlan {
   int pieces, piece;                        // per row; 8-token vectors of a piece
@@ -43,20 +43,23 @@ struct VerifyPlan {
 
 static VerifyPlan plan_verify(int batch, int rows, int vocab, int sms) {
   VerifyPlan p;
-  // about sixteen CTAs per SM (four or five run at once), at least 4096 tokens each (16 a thread)
+  // About sixteen CTAs per SM (four or five run at once); at least 8192 tokens each in the first launch (one
+  // round of 32 a thread), 2048 in the second (one round of 8).  One sequence of 4 drafts, 151936 tokens: 10.7 us
+  // with 4096 and 4096, 10.1 with 4096 and 2048, 9.4 with 8192 and 2048, 10.1 with 16384 and 2048, 9.5 with
+  // 8192 and 1024: rounds of a thread wait for memory one after the other, pieces are joined by every CTA.
   const long long want = 16LL * sms;
-  auto cut = [&](long long n, int most) {
+  auto cut = [&](long long n, int most, int least) {
     long long k = want / n;
-    const long long fit = (vocab + 4095) / 4096;
+    const long long fit = (vocab + least - 1) / least;
     if (k > fit) k = fit;
     if (k > most) k = most;
     return (int)(k < 1 ? 1 : k);
   };
   const int vecs = vocab / 8 + 1;
-  p.pieces = cut((long long)batch * rows, kVfMaxPieces);
+  p.pieces = cut((long long)batch * rows, kVfMaxPieces, 8192);
   p.piece = (vecs + p.pieces - 1) / p.pieces;
   p.pieces = (vecs + p.piece - 1) / p.piece;
-  p.parts = cut(4LL * batch, kVfMaxParts);
+  p.parts = cut(4LL * batch, kVfMaxParts, 2048);
   p.part = ((vocab + p.parts - 1) / p.parts + 7) & ~7;
   p.parts = (vocab + p.part - 1) / p.part;
   return p;
