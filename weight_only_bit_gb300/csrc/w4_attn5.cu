@@ -20,7 +20,7 @@
 // Roles (four warpgroups of 128 threads; registers move from the last to the first two), connected by
 // mbarriers:
 //   warps 0-3, 4-7   softmax of stream 0 and 1: a thread per row, one pass over its S, 64 keys at a time:
-//                    their maximum, then weights, sums, P.  Where a maximum passes the bound (the
+//                    their maximum (D = 128), then weights, sums, P.  Where the bound is passed (the
 //                    first keys of an item, rarely later), O is rescaled in place.  At the end out.
 //   warps 8-11       codes from global memory, FP16 into shared memory: keys in the canonical K-major
 //                    layout, values in the MN-major one (channels contiguous, as they lie in
@@ -28,8 +28,9 @@
 //   warps 12, 13     issue the MMAs of stream 0 and 1: the next S, then PV (the whole warp walks,
 //                    one elected lane issues: descriptors stay in uniform registers).  One warp for both
 //                    streams spent as long on waits and commits as the products take.
+//   warps 14, 15     q of stream 0 and 1 by TMA, an item ahead.
 // Measured (GB300): a causal prompt of 8191 tokens, 12 heads on 2, D = 128: 198 us, 1040 TFLOP/s, 53 % of
-// the measured FP16 rate.  8 chunks of up to 517 tokens, window 4096, 16 heads on 4, D = 64: 76 us.
+// the measured FP16 rate.  8 chunks of up to 517 tokens, window 4096, 16 heads on 4, D = 64: 72 us.
 // What bounds it: no unit alone.  A job pair (one of each stream) takes 2000 cycles: tensor pipe 1300
 // (S at 48 cycles an instruction of 64 keys, bound by shared memory reading q again each time; PV at 64),
 // maxima and exponentials of the two warps of a scheduler 1050, with hand-overs of 130 cycles each and
@@ -62,6 +63,8 @@ constexpr int kA5RegsSoftmax = 136, kA5RegsMma = 112;
 constexpr float kA5Slack = 6.f;
 constexpr int kA5ScaleSlots = 4;
 
+static_assert(sizeof(Walk<kA5T, kA5Ov>) <= 128, "a walk's place in shared memory");
+
 template <int D>
 struct A5Smem {
   static constexpr int kTile = 128 * D * 2;              // 128 rows of FP16: D / 64 blocks of 128 x 128 bytes
@@ -71,10 +74,11 @@ struct A5Smem {
   static constexpr int oScales = 6 * kTile;              // [slots][8 groups] (ks c, log2 vs, 1 / vs, 0)
   static constexpr int oMl = oScales + kA5ScaleSlots * 8 * 16;   // [128] (maximum, sum) of stream 1
   static constexpr int oBar = oMl + 128 * 8;
-  static constexpr int kBars = 2 + 2 + 2 + 2 + 2 + 2 + 4 + 2 + 4 + 1;
+  static constexpr int kBars = 2 + 2 + 2 + 2 + 2 + 2 + 4 + 2 + 4 + 2 + 1;
   static constexpr int oFlag = oBar + kBars * 8;
   static constexpr int oPrefix = oFlag + 16;
-  static constexpr int oOut = (oPrefix + (W4_MAX_SEQS + 1) * 4 + 15) & ~15;   // 8 softmax warps x 32 rows x 64 bytes
+  static constexpr int oWalk = (oPrefix + (W4_MAX_SEQS + 1) * 4 + 15) & ~15;   // 8 softmax warps
+  static constexpr int oOut = oWalk + 8 * 128;   // 8 softmax warps x 32 rows x 64 bytes
   static constexpr int kTotal = oOut + 8 * 2048 + 1024;
 };
 
@@ -254,7 +258,8 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
   uint64_t* pfull = sfree + 2;                                    // 4 softmax warps: P of (stream, place) is there
   uint64_t* qfull = pfull + 4;                                    // TMA: Q of the stream is there
   uint64_t* pvdone = qfull + 2;                                   // commit: O has taken in P of (stream, place)
-  uint64_t* done = pvdone + 4;
+  uint64_t* qempty = pvdone + 4;                                  // Q of the stream is not read any more
+  uint64_t* done = qempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::oFlag);
   int* flag = reinterpret_cast<int*>(smem + S::oFlag + 8);
   int* bad = flag + 1;                       // a softmax warp lost a wait: all of them leave together
@@ -268,6 +273,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
       mbar_init(&vfull[i], 4);
       mbar_init(&vempty[i], 2);
       mbar_init(&qfull[i], 1);
+      mbar_init(&qempty[i], 1);
       mbar_init(&sfull[i], 2);
       mbar_init(&sfree[i], 4);
     }
@@ -435,6 +441,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
             a5_commit(lead, &sfull[s]);
             if (lane == 0) a5_arrive(b_s);
             if (h > h0 || !two) a5_commit(lead, &kempty[st]);
+            if (two && h > 0 && tile == last) a5_commit(lead, &qempty[s]);
           };
           // PV of half h of a tile, P in place pl
           auto pv = [&](int tile, int h, int pl, uint32_t parity) {
@@ -480,6 +487,29 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
       };
       if (warp == kA5Mma) issue(A5Stream<0>{});
       if (warp == kA5Mma + 1) issue(A5Stream<1>{});
+      if (warp >= kA5Mma + 2 && lane == 0) {
+        // ---------------------------------------------------------------- q of a stream, by TMA, an item ahead
+        const int s = warp - kA5Mma - 2;
+        const uint32_t b_q = smem_u32(qfull + s), b_e = smem_u32(qempty + s);
+        uint32_t items = 0;
+        bool more = true;
+        while (more && ok) {
+          const Item& it = w.it;
+          const bool two = it.n - it.rb * tpb > p.tpt;
+          if (items > 0) ok = a5_wait(b_e, (items - 1) & 1, 0x52e);
+          if (!ok) break;
+          a5_fence_proxy();                          // the places may have held sums of an item
+          mbar_arrive_expect_tx(&qfull[s], (uint32_t)(p.tpt * p.group * D * 2));
+          const int t0 = it.start + it.rb * tpb + (two ? s * p.tpt : 0);
+#pragma unroll
+          for (int b = 0; b < D / 64; ++b)
+            a5_tma3(sb + S::oQ + s * S::kTile + b * 16384, &p.tq, 64 * b, it.h * p.group, t0, &qfull[s]);
+          ++items;
+          more = w.next(a, tpb);
+        }
+        a5_wait(b_q, (items - 1) & 1, 0x52f);        // (no copy in flight when the CTA ends)
+      }
+      __syncwarp();
     } else {
       // ================================================================ softmax
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kA5RegsSoftmax));
@@ -492,59 +522,42 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
                      b_pv = smem_u32(pvdone + 2 * s);
       uint32_t jobs = 0;                             // parity of sfull
       uint32_t turn[2] = {1, 1};                     // parities of the places' last products (none yet: complete)
-      bool more = true, asked = false;               // asked: this item's q is on its way
-      auto ask_q = [&](const Walk<kA5T, kA5Ov>& y) {
-        const Item& x = y.it;
-        const bool both = x.n - x.rb * tpb > p.tpt;
-        if (tr == 0) {
-          a5_fence_proxy();                                      // the places may have held sums of an item
-          mbar_arrive_expect_tx(&qfull[s], (uint32_t)(p.tpt * p.group * D * 2));
-          const int t0 = x.start + x.rb * tpb + (both ? s * p.tpt : 0);
-#pragma unroll
-          for (int b = 0; b < D / 64; ++b)
-            a5_tma3(sb + S::oQ + s * S::kTile + b * 16384, &p.tq, 64 * b, x.h * p.group, t0, &qfull[s]);
-        }
-      };
+      bool more = true;
+      Walk<kA5T, kA5Ov>* mine_w = reinterpret_cast<Walk<kA5T, kA5Ov>*>(smem + S::oWalk + warp * 128);
       while (more) {
-        const Item& it = w.it;
-        const bool two = it.n - it.rb * tpb > p.tpt;
-        const int i0 = it.rb * tpb + (two ? s * p.tpt : 0);      // the row tile's first token
+        // (the walk waits in shared memory: its registers are the jobs')
+        if (lane == 0) *mine_w = w;
+        __syncwarp();
+        const bool two = w.it.n - w.it.rb * tpb > p.tpt;
+        const int i0 = w.it.rb * tpb + (two ? s * p.tpt : 0);      // the row tile's first token
         const int n = w.u1 - w.u0;
-        if (!asked) ask_q(w);
-        asked = false;
         const int qi = i0 + tok;                                 // this row's token in the sequence
-        const bool valid = tok < p.tpt && qi < it.n;
-        const int pos = it.total - it.n + qi;
+        const bool valid = tok < p.tpt && qi < w.it.n;
+        const int pos = w.it.total - w.it.n + qi;
         // keys [rlo, rhi) that this row sees (rows beyond the item see all, and are not stored)
-        const int rhi = !valid ? 0x7fffffff : pos < 0 ? 0 : a.causal ? min(it.total, pos + 1) : it.total;
+        const int rhi = !valid ? 0x7fffffff : pos < 0 ? 0 : a.causal ? min(w.it.total, pos + 1) : w.it.total;
         const int rlo = !valid ? 0 : a.window > 0 ? pos - a.window + 1 : 0;
         float m = -INFINITY, l = 0.f;
         const int h0 = two ? 0 : s;                              // this stream's halves of a tile: both, or one
-        for (int q = h0; q < 2 * n; q += two ? 1 : 2) {          // jobs: 64 keys of a tile
-          const int h = q & 1, tile = q >> 1;
-          const int slot = (w.base + tile) & (kA5ScaleSlots - 1);
-          const int pl = two ? h : (w.base + tile) & 1;          // place of P: every second job the same
+        const int step = two ? 1 : 2, key0 = (w.it.t0 + w.u0) * kA5T, base0 = w.base;
+        float x[64];
+        // S of the next job on its way to registers
+        auto next_s = [&] {
           ok = ok && a5_wait(b_s, jobs, 0x52a);
           jobs ^= 1;
           t5_fence_after();
           __syncwarp();
-          float x[64];
           a5_ld32(ts, *reinterpret_cast<float(*)[32]>(&x[0]));
           a5_ld32(ts + 32, *reinterpret_cast<float(*)[32]>(&x[32]));
-          if (two && q == 2 * n - 1) {
-            // the item's products with q are complete: the next item's rows may come in
-            Walk<kA5T, kA5Ov> nx = w;
-            if (nx.next(a, tpb)) {
-              ask_q(nx);
-              asked = true;
-            }
-          }
-          const int k0 = (it.t0 + w.u0 + tile) * kA5T + h * 64;
+        };
+        next_s();
+        for (int q = h0; q < 2 * n; q += step) {                 // jobs: 64 keys of a tile
+          const int h = q & 1, tile = q >> 1;
+          const int slot = (base0 + tile) & (kA5ScaleSlots - 1);
+          const int pl = two ? h : (base0 + tile) & 1;          // place of P: every second job the same
+          const int k0 = key0 + q * 64;
           const uint32_t ssc = sb + S::oScales + slot * 128 + h * 64;
           const int clo = rlo - k0, chi = rhi - k0;              // columns that the row sees
-          float4 sc[4];
-#pragma unroll
-          for (int g = 0; g < 4; ++g) sc[g] = a5_lds_f4(ssc + g * 16);
           a5_wait32(*reinterpret_cast<float(*)[32]>(&x[0]));
           a5_wait32(*reinterpret_cast<float(*)[32]>(&x[32]));
           t5_fence_before();
@@ -555,72 +568,97 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < 64; ++i) x[i] = i >= clo && i < chi ? x[i] : -INFINITY;
           }
-          float mx = -INFINITY;
+          // the bound goes up to the largest logit where that passes it
+          auto lift = [&] {
+            float mx = -INFINITY;
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            float y = a5_max3(x[g * 16], x[g * 16 + 1], x[g * 16 + 2]);
-            float z = a5_max3(x[g * 16 + 3], x[g * 16 + 4], x[g * 16 + 5]);
-            y = a5_max3(y, x[g * 16 + 6], x[g * 16 + 7]);
-            z = a5_max3(z, x[g * 16 + 8], x[g * 16 + 9]);
-            y = a5_max3(y, x[g * 16 + 10], x[g * 16 + 11]);
-            z = a5_max3(z, x[g * 16 + 12], x[g * 16 + 13]);
-            y = a5_max3(y, x[g * 16 + 14], x[g * 16 + 15]);
-            y = fmaxf(y, z);
-            mx = fmaxf(mx, y == -INFINITY ? y : fmaf(y, sc[g].x, sc[g].y));
-          }
-          if (__any_sync(0xffffffffu, mx > m + kA5Slack)) {
-            // O goes over to the higher bound, once it has taken in every P before this one
-            const float nm = mx > m + kA5Slack ? mx : m;
-            const float al = nm == m ? 1.f : attn_ex2(m - nm);   // 0 where there was nothing
-            m = nm;
-            l *= al;
-            if (q > h0) {
-              ok = ok && a5_wait(b_pv + (pl ^ 1) * 8, pl ? turn[0] : turn[1], 0x52c);
-              t5_fence_after();
-              __syncwarp();
+            for (int g = 0; g < 4; ++g) {
+              float y = a5_max3(x[g * 16], x[g * 16 + 1], x[g * 16 + 2]);
+              float z = a5_max3(x[g * 16 + 3], x[g * 16 + 4], x[g * 16 + 5]);
+              y = a5_max3(y, x[g * 16 + 6], x[g * 16 + 7]);
+              z = a5_max3(z, x[g * 16 + 8], x[g * 16 + 9]);
+              y = a5_max3(y, x[g * 16 + 10], x[g * 16 + 11]);
+              z = a5_max3(z, x[g * 16 + 12], x[g * 16 + 13]);
+              y = a5_max3(y, x[g * 16 + 14], x[g * 16 + 15]);
+              y = fmaxf(y, z);
+              const float4 f = a5_lds_f4(ssc + g * 16);
+              mx = fmaxf(mx, y == -INFINITY ? y : fmaf(y, f.x, f.y));
+            }
+            if (__any_sync(0xffffffffu, mx > m + kA5Slack)) {
+              // O goes over to the higher bound, once it has taken in every P before this one
+              const float nm = mx > m + kA5Slack ? mx : m;
+              const float al = nm == m ? 1.f : attn_ex2(m - nm);   // 0 where there was nothing
+              m = nm;
+              l *= al;
+              if (q > h0) {
+                ok = ok && a5_wait(b_pv + (pl ^ 1) * 8, pl ? turn[0] : turn[1], 0x52c);
+                t5_fence_after();
+                __syncwarp();
 #pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                float v[32];
-                a5_get32(to + c, v);
-                uint32_t r0[16], r1[16];
+                for (int c = 0; c < D; c += 32) {
+                  float v[32];
+                  a5_get32(to + c, v);
+                  uint32_t r0[16], r1[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  r0[i] = __float_as_uint(v[i] * al);
-                  r1[i] = __float_as_uint(v[16 + i] * al);
+                  for (int i = 0; i < 16; ++i) {
+                    r0[i] = __float_as_uint(v[i] * al);
+                    r1[i] = __float_as_uint(v[16 + i] * al);
+                  }
+                  a5_st16(to + c, r0);
+                  a5_st16(to + c + 16, r1);
                 }
-                a5_st16(to + c, r0);
-                a5_st16(to + c + 16, r1);
               }
             }
-          }
-          const float base = m == -INFINITY ? 0.f : m;
+          };
+          // At D = 64 the usual job looks for no maximum: it takes the bound that there is, and its sums tell
+          // whether that held (16 weights of at most 2^12 in all; past it, once more from the logits).  Windowed
+          // chunks 75 -> 72 us.  At D = 128, with twice the codes to decode beside, every maximum is looked for:
+          // without, the softmax warps took the issue slots from the decoding ones (200 -> 212 us for a prompt).
+          bool lifted = D == 128 || __any_sync(0xffffffffu, m == -INFINITY);
+#pragma unroll 1
+          for (;;) {
+            if (lifted) lift();
+            float lj = 0.f, most = 0.f;
+            const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t pk[16];
+            for (int c = 0; c < 2; ++c) {
+              uint32_t pk[16];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const float4 f = a5_lds_f4(ssc + (2 * c + g) * 16);
-              const float2 kk = make_float2(f.x, f.x), bb = make_float2(f.y - base, f.y - base);
-              float2 sum = make_float2(0.f, 0.f);
+              for (int g = 0; g < 2; ++g) {
+                const float4 f = a5_lds_f4(ssc + (2 * c + g) * 16);
+                const float2 kk = make_float2(f.x, f.x), bb = make_float2(f.y - base, f.y - base);
+                float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                const int k = c * 32 + g * 16 + i;
-                const float2 e = a5_fma2(make_float2(x[k], x[k + 1]), kk, bb);
-                const float2 y = make_float2(attn_ex2(e.x), attn_ex2(e.y));
-                sum = a5_add2(sum, y);
-                pk[g * 8 + i / 2] = a5_pack(y.x, y.y);
+                for (int i = 0; i < 16; i += 2) {
+                  const int k = c * 32 + g * 16 + i;
+                  const float2 e = a5_fma2(make_float2(x[k], x[k + 1]), kk, bb);
+                  const float2 y = make_float2(attn_ex2(e.x), attn_ex2(e.y));
+                  sum = a5_add2(sum, y);
+                  pk[g * 8 + i / 2] = a5_pack(y.x, y.y);
+                }
+                const float s16 = sum.x + sum.y;
+                most = fmaxf(most, s16);
+                lj = fmaf(s16, f.z, lj);
               }
-              l = fmaf(sum.x + sum.y, f.z, l);
+              // (the place is free: the P before the last was taken in ahead of this job's S)
+              a5_st16(tp + pl * 32 + c * 16, pk);
             }
-            // (the place is free: the P before the last was taken in ahead of this job's S)
-            a5_st16(tp + pl * 32 + c * 16, pk);
+            if (lifted || !__any_sync(0xffffffffu, most > 4096.f)) {
+              l += lj;
+              break;
+            }
+            lifted = true;
+            a5_wait_st();
           }
           a5_wait_st();
           t5_fence_before();
           __syncwarp();
           if (lane == 0) a5_arrive(b_p + pl * 8);
+          if (q + step < 2 * n) next_s();
           if (pl) turn[1] ^= 1; else turn[0] ^= 1;
         }
+        w = *mine_w;
+        const Item& it = w.it;
         const bool whole = w.whole();
         const int c0 = whole ? cta : w.first_cta(sp), c1 = whole ? cta : w.last_cta(sp);
         unsigned int* ticket = reinterpret_cast<unsigned int*>(a.workspace) + c0;
@@ -783,6 +821,7 @@ __global__ void __launch_bounds__(kA5Threads, 1) w4_attn5_kernel(const __grid_co
         }
         if (!ok && lane == 0) *reinterpret_cast<volatile int*>(bad) = 1;
         a5_sync_softmax();                                       // Q's places and the flag are free again
+        if (!two && tr == 0) a5_arrive(smem_u32(qempty + s));
         if (*reinterpret_cast<volatile int*>(bad)) break;
         more = w.next(a, tpb);
       }
