@@ -29,7 +29,7 @@
 //                    one elected lane issues: descriptors stay in uniform registers).  One warp for both
 //                    streams spent as long on waits and commits as the products take.
 //   warps 14, 15     q of stream 0 and 1 by TMA, an item ahead.
-// Measured (GB300): a causal prompt of 8191 tokens, 12 heads on 2, D = 128: 198 us, 1040 TFLOP/s, 53 % of
+// Measured (GB300): a causal prompt of 8191 tokens, 12 heads on 2, D = 128: 199 us, 1035 TFLOP/s, 53 % of
 // the measured FP16 rate.  8 chunks of up to 517 tokens, window 4096, 16 heads on 4, D = 64: 72 us.
 // What bounds it: no unit alone.  A job pair (one of each stream) takes 2000 cycles: tensor pipe 1300
 // (S at 48 cycles an instruction of 64 keys, bound by shared memory reading q again each time; PV at 64),
